@@ -83,6 +83,7 @@ typedef enum {
     QMV_ERR_CUDA = -7,    /* a CUDA call or a kernel launch failed               */
     QMV_ERR_DEVICE = -8,  /* no usable CUDA device, or a device-side error was
                              recorded (see qmv_check)                            */
+    QMV_ERR_WS = -9,      /* the workspace is smaller than the call needs        */
 } qmv_status;
 
 #define QMV_MAX_NTOK 8
@@ -100,6 +101,10 @@ typedef enum {
                                        still land in shared memory reused by later
                                        kernels, so later results on this device are
                                        suspect (recreate the context to be sure)   */
+#define QMV_DEVERR_PAGE_ID 8        /* a block table named a page outside [0, n_pages);
+                                       its slots were left out (see kv_append ...) */
+#define QMV_DEVERR_SEQ_LEN 16       /* a sequence length was negative or beyond its
+                                       block table; it was clamped                 */
 
 /* y[rows] = W x.  x: f32 [cols]; y: f32 [rows].
  * One launch covers a whole fused projection: pass the row-concatenation of
@@ -267,6 +272,214 @@ int qmv_argmax_ws(int fmt, const void *W_blocks, int64_t rows, int64_t cols,
  * qmv_argmax_ws with separate workspaces for that). */
 int qmv_argmax(int fmt, const void *W_blocks, int64_t rows, int64_t cols,
                const float *x, float *y, int n_tok, int32_t *idx_out, qmv_stream_t stream);
+
+/* ------------------------------------------------- the key-value cache --
+ * Between the fused QKV projection and the O projection a decode step writes
+ * the new tokens' keys and values into a cache (kv_append), attends over it
+ * (attn_decode) and, where a sequence outgrows its budget, prunes it
+ * (kv_evict).  (Sources: BebeLM page, §独特的层设计 -- grouped-query attention
+ * layers, 32 query and 8 kv heads; FlareLLM page, §推理层面的深度优化 -- several
+ * tokens checked in one pass; the engines' KV caches.)
+ *
+ * The cache is a pool of pages.  A page holds page_size slots, a slot one
+ * token's key and value of every kv head.  A sequence's slots 0, 1, 2, ... lie
+ * in the pages that its row of the block table names, page_size slots each.
+ * Value i of kv head h of the slot at place o of page p is element
+ *     p * page_stride + h * head_stride + o * slot_stride + i
+ * of `k` (and of `v`), strides in values, so [page][head][slot][value] and
+ * [page][slot][head][value] pools are both usable, and so are pools with gaps.
+ *   QMV_KV_F16, QMV_KV_BF16: 16-bit floats; head_dim a multiple of 16, 16 to
+ *                 256; strides multiples of 8.
+ *   QMV_KV_Q8_0:  int8 quants in k / v, in blocks of 32 with an IEEE binary16
+ *                 scale each, value = scale * quant (the Q8_0 arithmetic; the
+ *                 scales lie apart so that quants keep 16-byte alignment): the
+ *                 scale of element e is element e / 32 of k_scale / v_scale.
+ *                 head_dim 64, 128, 192 or 256; strides multiples of 64.
+ * k, v: 16-byte aligned; scales: 4-byte aligned (NULL for the 16-bit types).
+ *
+ * Block tables are int32 [n_seq][table_stride] on the device; a sequence may
+ * use its first max_pages entries.  kv_len is int32 [n_seq] on the device.  So
+ * lengths and tables may change between replays of a captured graph.  An entry
+ * that a call reads must lie in [0, n_pages): slots of one that does not are
+ * left out (not read, not written, not attended) and QMV_DEVERR_PAGE_ID is
+ * recorded.  Entries whose slots a call does not touch are never read as pages
+ * (pages behind a sliding window may have been freed).  A length below 0 or above
+ * max_pages * page_size is clamped and QMV_DEVERR_SEQ_LEN recorded.
+ * Sequences may share pages that no call writes.
+ */
+typedef enum { QMV_KV_F16 = 0, QMV_KV_BF16 = 1, QMV_KV_Q8_0 = 2 } qmv_kv_type;
+
+typedef struct {
+    int32_t type;           /* qmv_kv_type                                      */
+    int32_t n_kv_head;      /* 1 .. 1024                                        */
+    int32_t head_dim;
+    int32_t page_size;      /* slots per page, >= 1                             */
+    int64_t n_pages;        /* pages of the pool, 1 .. 2^31 - 1                 */
+    int64_t page_stride, head_stride, slot_stride;
+    void *k, *v;            /* device                                           */
+    void *k_scale, *v_scale;
+} qmv_kv_cache;
+
+#define QMV_MAX_SEQ 1024            /* sequences of one call                    */
+#define QMV_ROPE_HALVES 0           /* pairs (i, i + rope_dim / 2)              */
+#define QMV_ROPE_PAIRS 1            /* pairs (2i, 2i + 1)                       */
+
+/* The new tokens into the cache, with their rotary embedding:
+ *   angle = pos * inv_freq[i], i < rope_dim / 2;  a' = a cos - b sin,
+ *   b' = a sin + b cos for every pair (a, b) of the first rope_dim values of
+ *   every q and k head (angles, sine and cosine in 64 bits, so that far
+ *   positions keep their phase; rounded once to f32, then to the cache's type)
+ *   Q8_0 blocks: scale = f16(min(amax / 127, 65504)), quant = value / scale
+ *   rounded to even and clamped to +-127, 0 where the scale is 0.
+ * Token t (0 <= t < n_tok) of sequence s goes to slot kv_len[s] - n_tok + t
+ * (kv_len counts the new tokens already) at position pos[s * n_tok + t], or at
+ * its slot number where pos is NULL.  A token whose slot is negative (a padded
+ * batch) or whose page is bad is not stored; its rotated q is written all the same.
+ * q, k, v: f32, token s * n_tok + t at + (s * n_tok + t) * stride floats, its heads
+ * one after another: rows of a fused QKV product are read as they lie (q = y,
+ * k = y + n_head * head_dim, all three strides the row length).  q_out: f32,
+ * same layout with q_out_stride; q == q_out with equal strides rotates in place;
+ * they may not overlap otherwise.  q and q_out may both be NULL.
+ * inv_freq: device f32 [rope_dim / 2], 0 <= rope_dim <= head_dim, even; with
+ * rope_dim 0 it may be NULL and values are stored as they are.
+ * All float pointers 4-byte aligned.  Two tokens of one call may not name the
+ * same slot of the same page. */
+typedef struct {
+    qmv_kv_cache cache;
+    const float *q, *k, *v;
+    float *q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    int32_t n_head, n_seq, n_tok;               /* n_head 1 .. 8192; n_tok 1 .. 8 */
+    int32_t rope_dim, rope_style;
+    int32_t max_pages;
+    int64_t table_stride;
+    const int32_t *block_table, *kv_len, *pos;
+    const float *inv_freq;
+} qmv_append;
+
+int kv_append(const qmv_append *a, qmv_stream_t stream);
+
+/* Attention of each sequence's newest n_tok tokens over its cache.  Query t of
+ * sequence s sits at slot p = kv_len[s] - n_tok + t and sees slot j when
+ *   j <= p  and  (window == 0  or  j > p - window  or  j < n_sink):
+ * causal, with a sliding window of `window` slots (the query's own counted)
+ * and the first n_sink slots visible throughout.  For query head h, which
+ * reads kv head h / (n_head / n_kv_head):
+ *   s_j = scale * q . k_j,   out = sum_j softmax(s)_j v_j   over the visible j.
+ * A query that sees nothing (p < 0, or bad pages only) yields zeros, and so
+ * does one whose every score is -infinity.  Values in
+ * slots that a query does not see never reach its result, NaN and infinities
+ * included; the visible values and q have to be finite.
+ * score != NULL: the weights are accumulated per slot and kv head for kv_evict,
+ *   score[s][h][j] += sum over the group's query heads and the n_tok queries of
+ *   softmax(s)_j,  f32, entry (s * n_kv_head + h) * score_stride + j;
+ * the entries of the newest n_tok slots are set, not added to, so a new slot
+ * needs no clearing; entries of slots that no query sees stay as they are.
+ * q, out: f32, 16- and 4-byte aligned, token s * n_tok + t at + (s * n_tok + t) *
+ * stride floats (q_stride a multiple of 4), heads one after another; n_head a
+ * multiple of n_kv_head, 1 <= n_head / n_kv_head * n_tok <= 1024.
+ * Sums, maxima and products are f32; q and the weights reach the tensor cores
+ * as exact sums of two f16 or three bf16 parts, so that no bits of f32 are lost.
+ * The work of all sequences and heads is cut into equal shares, one per CTA;
+ * sequences that several CTAs share are joined by the last one to finish, in a fixed
+ * order: results do not vary from run to run.
+ * workspace: attn_ws_bytes() of caller-owned device memory, 256-byte aligned,
+ * zero before the first call; every completed call leaves its counters zero
+ * again.  It may serve calls of other shapes it is large enough for; calls that may overlap on
+ * the GPU need workspaces of their own.  max_pages bounds the
+ * lengths that a captured graph may later see. */
+typedef struct {
+    qmv_kv_cache cache;
+    const float *q;
+    float *out, *score;
+    int64_t q_stride, out_stride, score_stride;
+    int32_t n_head, n_seq, n_tok, max_pages;
+    int64_t table_stride;
+    const int32_t *block_table, *kv_len;
+    float scale;
+    int32_t window, n_sink;
+    void *workspace;
+    size_t workspace_bytes;
+} qmv_attn;
+
+int attn_decode(const qmv_attn *a, qmv_stream_t stream);
+
+/* Workspace bytes of attn_decode for these sizes (with_score: score != NULL);
+ * 0 when the sizes are outside its limits.  Needs no device. */
+size_t attn_ws_bytes(const qmv_kv_cache *cache, int n_head, int n_seq, int n_tok, int max_pages,
+                     int with_score);
+
+/* A smaller cache for each sequence, kv head by kv head: of the kv_len[s]
+ * slots, the first keep_first, the last keep_last and, of the slots between,
+ * the ones with the highest score (ties: the lower slot; NaN counts as lowest),
+ * `budget` slots in all; all of them when kv_len[s] <= budget.  The kept slots
+ * are copied in their old order to slots 0, 1, ... of the pages that dst_table
+ * names, in the same pool.  The copy is never in place, because pages may be shared
+ * between sequences: no destination page may be a source page of the call or
+ * appear twice.  Then
+ *   kept[s][h][i]      = the old slot of new slot i   int32 [n_seq][n_kv_head][budget]
+ *   score_out[s][h][i] = its score                    f32, as score, with score_out_stride
+ *   len_out[s]         = min(kv_len[s], budget)       int32 [n_seq]
+ * Entries and slots behind the new length are left as they were.  score_out may not
+ * overlap score, nor len_out kv_len.  Slots of bad source pages
+ * take part in the choice but their values are not copied; bad destination
+ * pages are not written. */
+typedef struct {
+    qmv_kv_cache cache;
+    const float *score;
+    float *score_out;
+    int64_t score_stride, score_out_stride;     /* >= the slots used            */
+    int32_t n_seq, max_pages, dst_max_pages;
+    int32_t keep_first, keep_last, budget;      /* keep_first + keep_last <= budget,
+                                                   1 <= budget <= dst_max_pages * page_size */
+    int64_t table_stride, dst_table_stride;
+    const int32_t *block_table, *kv_len, *dst_table;
+    int32_t *kept, *len_out;
+} qmv_evict;
+
+int kv_evict(const qmv_evict *a, qmv_stream_t stream);
+
+/* Penalties, biases and a grammar mask on logits, and the greedy choice, beside
+ * qmv_argmax (which chooses from the plain product).  For row r and token v,
+ * with c = how often v occurs in hist[r][0 .. hist_len[r]) and the row's
+ * params[r] = { repetition, frequency, presence }, in f32, each step rounded:
+ *   z = logits[r][v];
+ *   if c > 0:  z = z > 0 ? z / repetition : z * repetition;
+ *              z = z - (frequency * c + presence);
+ *   z = z + bias      (bias_vals[r][i] of the last i < bias_len[r] with
+ *                      bias_ids[r][i] == v; no entry: nothing is added);
+ *   z = -infinity where bit v % 32 of mask[r][v / 32] is 0.
+ * out[r][v] = z (out may be logits, with the same stride, or NULL) and
+ * idx_out[r] = the lowest v among the largest z of the tokens that the mask
+ * lets through, NaN and -infinity left out, -1 when none is left.
+ * Ids outside [0, vocab) in hist and bias_ids are skipped.  hist, bias_* and
+ * mask may be NULL (nothing to apply); hist needs hist_len and params; the
+ * strides are in elements, hist_len and bias_len are device int32 [n_rows] and are clamped to
+ * [0, stride].  logits, out, bias_vals, params: f32, 4-byte aligned.
+ * workspace: logits_ws_bytes(n_rows) device bytes, 8-byte aligned, zero before
+ * the first call and left zero by every completed call; calls that may overlap
+ * need their own. */
+typedef struct {
+    const float *logits;
+    float *out;
+    int64_t logits_stride, out_stride;
+    int32_t n_rows;                             /* 1 .. 65535                   */
+    int32_t vocab;                              /* 1 .. 2^31 - 1                */
+    const int32_t *hist, *hist_len;
+    int64_t hist_stride;
+    const float *params;                        /* [n_rows][3]                  */
+    const int32_t *bias_ids, *bias_len;
+    const float *bias_vals;
+    int64_t bias_stride;
+    const uint32_t *mask;
+    int64_t mask_stride;                        /* words                        */
+    int32_t *idx_out;                           /* [n_rows]                     */
+    void *workspace;
+    size_t workspace_bytes;
+} qmv_logits;
+
+int logits_argmax(const qmv_logits *a, qmv_stream_t stream);
+size_t logits_ws_bytes(int n_rows);
 
 /* Dequantize the whole matrix to f32: out[rows][cols].  The values are
  * bit-exact f32 evaluations of the block formulas above (every product in

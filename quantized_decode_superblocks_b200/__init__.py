@@ -21,14 +21,16 @@ LIB_PATH = os.path.join(_HERE, "libqmv.so")
 QMV_OK = 0
 STATUS_NAMES = {0: "QMV_OK", -1: "QMV_ERR_NULL", -2: "QMV_ERR_FMT", -3: "QMV_ERR_SHAPE",
                 -4: "QMV_ERR_ALIGN", -5: "QMV_ERR_NTOK", -6: "QMV_ERR_NSEL", -7: "QMV_ERR_CUDA",
-                -8: "QMV_ERR_DEVICE"}
+                -8: "QMV_ERR_DEVICE", -9: "QMV_ERR_WS"}
 DEVERR_EXPERT_ID = 1
 DEVERR_TIMEOUT = 2
 DEVERR_DRAIN = 4
+DEVERR_PAGE_ID = 8
+DEVERR_SEQ_LEN = 16
 KERNEL_WARP_RING, KERNEL_GENERAL, KERNEL_TENSOR_CORE, KERNEL_STREAM = 1, 2, 3, 4
 
 EXPORTED = ("qmv_f32", "qmv_batched", "qmv_multi", "qmv_chain", "qmv_argmax", "qmv_argmax_ws", "moe_route", "moe_qmv", "moe_ffn", "moe_ffn_routed", "moe_ffn_static",
-            "qmv_dequant",
+            "qmv_dequant", "kv_append", "attn_decode", "attn_ws_bytes", "kv_evict", "logits_argmax", "logits_ws_bytes",
             "qmv_check", "qmv_strerror", "qmv_block_bytes", "qmv_block_weights",
             "qmv_debug_fail_next_launches", "qmv_debug_short_copies", "qmv_set_pdl", "qmv_get_pdl",
             "qmv_last_cuda_error", "qmv_debug_last_kernel")
@@ -48,6 +50,10 @@ class QmvError(RuntimeError):
             detail += ": " + lib().qmv_last_cuda_error().decode()
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)} ({detail})")
 
+
+from .step import (AppendArgs, AttnArgs, EvictArgs, KV_BF16, KV_F16, KV_Q8_0, KvCache,  # noqa: E402,F401
+                   LogitsArgs, ROPE_HALVES, ROPE_PAIRS, attn_decode, attn_ws_bytes, kv_append, kv_evict,
+                   logits_argmax, logits_ws_bytes)
 
 _lib = None
 
@@ -75,6 +81,12 @@ def lib() -> ctypes.CDLL:
         L.moe_ffn_static.argtypes = [c_int, vp, vp, i64, c_int, vp, i64, c_int, vp, vp, c_int, i64, i64,
                                      vp, vp, vp]
         L.qmv_dequant.argtypes = [c_int, vp, i64, i64, vp, vp]
+        L.kv_append.argtypes = [ctypes.POINTER(AppendArgs), vp]
+        L.attn_decode.argtypes = [ctypes.POINTER(AttnArgs), vp]
+        L.attn_ws_bytes.argtypes = [ctypes.POINTER(KvCache), c_int, c_int, c_int, c_int, c_int]
+        L.kv_evict.argtypes = [ctypes.POINTER(EvictArgs), vp]
+        L.logits_argmax.argtypes = [ctypes.POINTER(LogitsArgs), vp]
+        L.logits_ws_bytes.argtypes = [c_int]
         L.qmv_check.argtypes = [vp, ctypes.POINTER(c_int)]
         L.qmv_strerror.argtypes = [c_int]
         L.qmv_strerror.restype = ctypes.c_char_p
@@ -91,8 +103,9 @@ def lib() -> ctypes.CDLL:
         L.qmv_debug_last_kernel.argtypes = []
         L.qmv_last_cuda_error.argtypes = []
         L.qmv_last_cuda_error.restype = ctypes.c_char_p
+        L.attn_ws_bytes.restype = L.logits_ws_bytes.restype = ctypes.c_size_t
         for name in EXPORTED:
-            if name not in ("qmv_strerror", "qmv_block_bytes", "qmv_debug_fail_next_launches",
+            if name not in ("attn_ws_bytes", "logits_ws_bytes", "qmv_strerror", "qmv_block_bytes", "qmv_debug_fail_next_launches",
                             "qmv_debug_short_copies", "qmv_set_pdl", "qmv_last_cuda_error"):
                 getattr(L, name).restype = c_int
         _lib = L

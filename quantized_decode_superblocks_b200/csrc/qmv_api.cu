@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "../../include/qmv.h"
+#include "qmv_host.h"
 #include "qmv_misc.cuh"
 #include "qmv_rw.cuh"
 #include "qmv_sk.cuh"
@@ -747,6 +748,25 @@ int argmax_check(int fmt, const void *W, int64_t rows, int64_t cols, const float
 
 }  // namespace
 
+namespace qmv {
+
+int host_dev(HostDev &out)
+{
+    DevInfo di;
+    const int rc = get_dev(di);
+    if (rc == QMV_OK) {
+        out.sm_count = di.sm_count;
+        out.err = di.err;
+    }
+    return rc;
+}
+
+int host_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+
+bool host_injected_failure() { return injected_failure(); }
+
+}  // namespace qmv
+
 extern "C" {
 
 size_t qmv_block_bytes(int fmt) { return (size_t)block_bytes(fmt); }
@@ -779,6 +799,7 @@ const char *qmv_strerror(int status)
     case QMV_ERR_NSEL: return "n_sel / top_k / n_expert outside the supported range";
     case QMV_ERR_CUDA: return "a CUDA call or kernel launch failed";
     case QMV_ERR_DEVICE: return "no usable sm_100 device, or a device-side error was recorded";
+    case QMV_ERR_WS: return "the workspace is smaller than the call needs";
     default: return "unknown status";
     }
 }
