@@ -8,27 +8,34 @@
 // Two parts (m, l, o) of one row join as m = max, l and o scaled by 2^(m_i - m)
 // and added; out = o / l.
 //
-// Work split.  The cache is cut into tiles of 16 slots of one kv head.  The
-// tiles of all sequences, heads and row blocks are numbered through, and CTA c
-// takes the c-th equal range of them, so that ragged batches and single long
+// Work split.  The cache is cut into tiles of 16 slots of one kv head, 4 of them
+// (one per warp) are a step.  The steps of all sequences, heads and row blocks
+// are numbered through, and CTA c takes the c-th equal range of them, so that ragged batches and single long
 // sequences load every SM alike; the lengths are only known on the device, so
 // every CTA finds its own range from a prefix sum over them.  A (sequence, row
 // block, head) that lies in several ranges leaves its parts in the workspace,
 // and the last of its CTAs to arrive (a counter) joins them in CTA order.
+// Two CTAs share an SM where shared memory allows, so that one streams while
+// the other starts or joins a segment.
 //
-// In a CTA, warp w streams every 8th tile through a ring of its own
+// In a CTA, each of 4 warps streams every 4th tile through a ring of its own
 // (cp.async, NST stages) and multiplies on the tensor cores (m16n8k16, f32
-// accumulation).  The 16 rows of a product are 8 query rows twice: the upper
-// half holds the leading part of the f32 operand, the lower half the rest,
+// accumulation) with the cache as the A operand:
+//   S^T[16 slots][8 rows] = K q^T,   O^T[16 dims][8 rows] += V^T P^T,
+// so a fragment of K or V is loaded (and, for Q8_0, unpacked) once for all rows
+// of the CTA, and 8 rows fill the instruction.  The weights turn from the first
+// product's C layout to the second's B layout by movmatrix.  f32 operands are
+// split into parts that the tensor core multiplies exactly:
 //   f16 cache:   q * 2^e (per row, so that the largest value is below 2^13) and
-//                2^15 * p as two f16 parts: 22 bits, absolute error 2^-23 of
-//                the row's largest value;
-//   bf16 and Q8_0 cache (int8 is exact in both): p (and q for bf16) as three
-//                bf16 parts, 24 bits; the third part is a product of its own.
-// so one thread holds both halves of its scores and of its outputs and adds
-// them without a shuffle, and p of one product is the A operand of the next.
-// With more than 8 rows, mt warps form a group that shares its mt tiles: each
-// loads one and multiplies all of them with its own 8 rows.
+//                2^9 * p as two f16 parts: 22 bits;
+//   bf16 cache:  q and p as three bf16 parts, 24 bits;
+//   Q8_0 cache:  q as for f16 (int8 is exact in f16), p * scale as for bf16.
+// Tensor cores cut off the bits that an accumulation shifts out, so a long chain of
+// them drifts: each tile's product starts from zero and is added to the
+// running output by rounded f32 adds.
+//
+// The running maximum m is a reference: it only moves when a score passes it by
+// more than a slack, so most tiles need no reduction across lanes.
 //
 // Slots that no query of the call sees are not loaded (their shared memory is
 // zeroed by the copy).  A slot that only some of several queries see is kept out of
@@ -45,11 +52,18 @@ namespace qmv {
 
 enum { KV_F16 = 0, KV_BF16 = 1, KV_Q8_0 = 2 };
 
-constexpr int ATT_NW = 8;                    // warps of a CTA (at most; see AttnGeom)
+constexpr int ATT_NW = 4;                    // warps of a CTA
+constexpr int ATT_THREADS = ATT_NW * 32;
 constexpr int ATT_TILE = 16;                 // slots of a tile
+// log2 of how far a weight may pass 1, and of the factor of the weights in f16
+// parts: together below 2^16, and the second keeps what an f16 part cuts off
+// (half a step of its subnormals) below 2^-34 of the reference.  bf16 parts
+// have f32's range.
+__host__ __device__ constexpr float attn_slack(int type) { return type == 0 ? 6.f : 12.f; }
+constexpr float ATT_F16_SHIFT = 9.f;
 
-// 8-row blocks that one CTA takes: up to 4, 2 where q's fragments lie in shared memory
-__host__ __device__ constexpr int attn_max_mt(int dim) { return dim <= 128 ? 4 : 2; }
+// 8-row blocks that one CTA takes at most: the outputs of 4 (2) of them fill half its registers
+__host__ __device__ constexpr int attn_max_mb(int dim) { return dim <= 128 ? 4 : 2; }
 constexpr int ATT_MAX_SEQ = 1024;
 constexpr int ATT_MAX_CTAS = 320;            // bound for the workspace's parts
 
@@ -64,13 +78,14 @@ struct AttnParams {
     int64_t table_stride, n_pages;
     int32_t n_seq, n_tok, n_kv, group, rows, dim;        // rows = n_tok * group
     int32_t page_size, page_shift, max_len;              // page_shift < 0: not a power of two
-    int32_t mt, n_rb;                                    // 8-row blocks of a CTA, row blocks of a head
-    int32_t window, n_sink, min_tiles;
+    int32_t mb, n_rb;                                    // 8-row blocks of a CTA, row blocks of a head
+    int32_t window, n_sink;
     float scale_log2, l_shift;                           // l counts 2^l_shift times the weights
     unsigned *counters;                                  // [ATT_MAX_CTAS], zero between calls
-    float *part_ml, *part_o;                             // [2 * CTAs][8 mt][2], [..][dim]
-    float *raw, *stats;                                  // scores s and (m, l) of every row, for `score`
-    int64_t raw_stride;
+    float *part_ml, *part_o;                             // [2 * CTAs][8 mb][2], [..][dim]
+    float *raw, *stats;                                  // scores s [..][slot][row] and (m, l) of every row, for `score`
+    int64_t raw_stride;                                  // slots
+    int32_t raw_rows;                                    // rows, made even
     int *err;
 };
 
@@ -79,7 +94,7 @@ struct AttnSeq {
     int len, first;        // length; slot of the first query (may be negative)
     int lo, sinks;         // slots >= lo, and slots < sinks, are seen by some query
     int sink_tiles, base;  // tiles 0 .. sink_tiles - 1 start at slot 0, the others at slot base
-    int n_tiles;           // at least 1, so that every row gets written
+    int n_tiles, n_steps;  // at least 1, so that every row gets written
 
     __device__ __forceinline__ void set(int n, const AttnParams &p)
     {
@@ -94,12 +109,18 @@ struct AttnSeq {
             if (sinks > 0 && sink_tiles * ATT_TILE >= base) sink_tiles = base = 0;   // the parts meet
         }
         n_tiles = max(1, sink_tiles + (len - base + ATT_TILE - 1) / ATT_TILE);
+        n_steps = (n_tiles + ATT_NW - 1) / ATT_NW;
     }
     __device__ __forceinline__ int slot0(int tile) const
     {
         return tile < sink_tiles ? tile * ATT_TILE : base + (tile - sink_tiles) * ATT_TILE;
     }
     __device__ __forceinline__ bool seen(int j) const { return j < len && (j >= lo || j < sinks); }
+    // Slots j0 .. j0 + 15 are seen by every query (of several).
+    __device__ __forceinline__ bool by_all(int j0, const AttnParams &p) const
+    {
+        return j0 + ATT_TILE - 1 <= first && (p.window == 0 || j0 > len - 1 - p.window || j0 + ATT_TILE <= p.n_sink);
+    }
 };
 
 __device__ __forceinline__ int attn_len(const AttnParams &p, int s)
@@ -147,6 +168,26 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+template <bool BF16>
+__device__ __forceinline__ void mma_16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF16) mma_bf16(c, a[0], a[1], a[2], a[3], b0, b1);
+    else mma_f16(c, a[0], a[1], a[2], a[3], b0, b1);
+}
+// An 8x8 matrix of 16-bit values, two of a row per lane, transposed.
+__device__ __forceinline__ uint32_t movm_t(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // (x, y) as two f16 parts / three bf16 parts, packed pairwise.
 __device__ __forceinline__ void split_f16(float x, float y, uint32_t &hi, uint32_t &lo)
 {
@@ -156,17 +197,27 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t &hi, uint32
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
+// Each part is the leading 8 bits of what is left (cut off, not rounded: the
+// rest of 24 bits always fits the next two).
 __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo)
 {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    const float2 f = __bfloat1622float2(h);
-    const float rx = x - f.x, ry = y - f.y;
-    const __nv_bfloat162 m = __floats2bfloat162_rn(rx, ry);
-    const float2 g = __bfloat1622float2(m);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(rx - g.x, ry - g.y);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    mid = *reinterpret_cast<const uint32_t *>(&m);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
+    const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
+    hi = __byte_perm(ux, uy, 0x7632);
+    const float rx = x - __uint_as_float(ux & 0xFFFF0000u), ry = y - __uint_as_float(uy & 0xFFFF0000u);
+    const uint32_t vx = __float_as_uint(rx), vy = __float_as_uint(ry);
+    mid = __byte_perm(vx, vy, 0x7632);
+    lo = __byte_perm(__float_as_uint(rx - __uint_as_float(vx & 0xFFFF0000u)), __float_as_uint(ry - __uint_as_float(vy & 0xFFFF0000u)), 0x7632);
+}
+// (a, b) += (x, y) and (a, b) *= (x, y), one instruction each.
+__device__ __forceinline__ void add2(float &a, float &b, float x, float y)
+{
+    asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void mul2(float &a, float &b, float x, float y)
+{
+    asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
 }
 
 // Four int8 of a word as two pairs of exact f16: the byte, its sign bit
@@ -193,8 +244,8 @@ __device__ __forceinline__ void i8_to_bf16(uint32_t w, uint32_t &p02, uint32_t &
     p13 = *reinterpret_cast<const uint32_t *>(&y);
 }
 
-// Shared-memory geometry of one instance.
-template <int TYPE, int DP>
+// Shared-memory geometry of one instance: MB 8-row blocks of a DP-wide head.
+template <int TYPE, int DP, int MB>
 struct AttnGeom {
     static constexpr int EB = TYPE == KV_Q8_0 ? 1 : 2;           // bytes of a value
     static constexpr int PITCH = DP * EB;                        // bytes of a slot's k (or v)
@@ -203,22 +254,21 @@ struct AttnGeom {
     static constexpr int SC_PITCH = DP / 32 * 2;                 // a slot's scales
     static constexpr int SC_BYTES = TYPE == KV_Q8_0 ? ATT_TILE * SC_PITCH : 0;
     static constexpr int STAGE = 2 * (KV_BYTES + SC_BYTES);      // one warp's stage: k | v | k scales | v scales
-    // Warps and stages: 130 to 200 KB of ring per SM.
-    static constexpr int NW = STAGE > 12 * 1024 ? 4 : ATT_NW;
-    static constexpr int THREADS = NW * 32;
-    static constexpr int NST = STAGE >= 8 * 1024 ? 3 : STAGE >= 4 * 1024 ? 4 : 6;
-    static constexpr int RING = NW * NST * STAGE;
-    static constexpr int MAX_MT = attn_max_mt(DP);
-    static constexpr bool QREG = DP <= 128;                      // q's operand fragments in registers
-    static constexpr int NPART = TYPE == KV_BF16 ? 3 : 2;        // words of q per k-step and k half
-    static constexpr int QS_WORDS = 2 * NPART;                   // per lane and k-step
-    static constexpr int Q_BYTES = QREG ? 0 : MAX_MT * (DP / 16) * 32 * QS_WORDS * 4;
-    static constexpr int OPITCH = DP + 8;                        // floats: the 8 rows of a store in different banks
-    static_assert(NW * 8 * OPITCH * 4 <= RING, "the warps' outputs are joined in the ring");
-    static_assert(ATT_MAX_CTAS * 8 * MAX_MT * 4 <= RING, "the parts' factors lie in the ring");
+    static constexpr int ROWS = 8 * MB;
+    // Stages: about 96 KB of ring a CTA, two CTAs a SM (one where a stage is 16 KB).
+    static constexpr int NST = STAGE >= 8 * 1024 ? 3 : STAGE >= 4 * 1024 ? 5 : 8;
+    static constexpr int RING = ATT_NW * NST * STAGE;
+    static constexpr int NPQ = TYPE == KV_BF16 ? 3 : 2;          // parts of q
+    static constexpr int NPP = TYPE == KV_F16 ? 2 : 3;           // parts of the weights
+    static constexpr bool QREG = MB == 1 && DP <= 128;           // q's operand fragments in registers
+    static constexpr int QW = 2 * NPQ;                           // words of q per lane and 16 columns
+    static constexpr int Q_BYTES = QREG ? 0 : MB * (DP / 16) * 32 * QW * 4;
+    static constexpr int OPITCH = DP + 4;                        // floats: a store's rows in different banks
+    static_assert(ATT_NW * ROWS * OPITCH * 4 <= RING, "the warps' outputs are joined in the ring");
     static constexpr int SMEM = RING + Q_BYTES;
-    static_assert(SMEM + 6 * 1024 <= 227 * 1024, "one CTA's shared memory");
-    // 16-byte chunk c of row r, so that 8 rows' chunks fall in different banks
+    static constexpr int CTAS = SMEM <= 110 * 1024 ? 2 : 1;      // on a SM
+    static_assert(SMEM <= 222 * 1024, "one CTA's shared memory");
+    // 16-byte chunk c of slot r, so that 8 slots' chunks fall in different banks
     static __device__ __forceinline__ uint32_t at(int r, int c)
     {
         const int x = NCHUNK >= 8 ? (r & 7) : ((r >> 1) & 3);
@@ -226,25 +276,26 @@ struct AttnGeom {
     }
 };
 
-template <int TYPE, int DP>
-__global__ void __launch_bounds__(AttnGeom<TYPE, DP>::THREADS, 1) attn_decode_kernel(const __grid_constant__ AttnParams p)
+template <int TYPE, int DP, int MB>
+__global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) attn_decode_kernel(const __grid_constant__ AttnParams p)
 {
-    using G = AttnGeom<TYPE, DP>;
-    constexpr int NW = G::NW, NT = G::THREADS;
+    using G = AttnGeom<TYPE, DP, MB>;
+    constexpr int NW = ATT_NW, NT = ATT_THREADS, NPQ = G::NPQ, NPP = G::NPP, QW = G::QW;
+    constexpr bool PBF = TYPE != KV_F16;                         // type of the second product's parts
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int s_pref[ATT_MAX_SEQ + 1];                      // tiles of one head before each sequence
+    __shared__ int s_pref[ATT_MAX_SEQ + 1];                      // steps of one head before each sequence
     __shared__ int s_warp[NW];
-    __shared__ float s_m[NW][8], s_l[NW][8];
-    __shared__ float s_mr[8 * G::MAX_MT], s_lr[8 * G::MAX_MT];
-    __shared__ uint32_t s_mask[NW][G::NST];                       // per warp and stage: slots to use
+    __shared__ float s_m[NW][G::ROWS], s_l[NW][G::ROWS];
+    __shared__ float s_lr[G::ROWS], s_sf[G::ROWS];
+    __shared__ int s_at[G::ROWS];                                // the slot of each row's query, -1 for rows past the end
+    __shared__ uint32_t s_mask[NW][G::NST];                      // per warp and stage: slots to use
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c4 = lane & 3;
-    const int mt = p.mt, kg = warp / mt, mi = warp % mt;         // key group, row block in it
     const uint32_t ring0 = smem_addr(smem);
     const int units = p.n_rb * p.n_kv;
 
-    // ---- where this CTA's tiles lie: prefix sum of the sequences' tiles
+    // ---- where this CTA's steps lie: prefix sum of the sequences' steps
     {
         int run = 0;
         for (int s0 = 0; s0 < p.n_seq; s0 += NT) {
@@ -254,8 +305,8 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP>::THREADS, 1) attn_decode_ke
                 const int raw = __ldg(p.kv_len + s);
                 if ((raw < 0 || raw > p.max_len) && blockIdx.x == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
                 AttnSeq q;
-                q.set(attn_len(p, s), p);
-                n = q.n_tiles;
+                q.set(min(max(raw, 0), p.max_len), p);
+                n = q.n_steps;
             }
             int x = n;
             for (int o = 1; o < 32; o <<= 1) {
@@ -275,129 +326,124 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP>::THREADS, 1) attn_decode_ke
         }
         if (tid == 0) s_pref[p.n_seq] = run;
     }
-    if (p.dim < DP) {      // columns behind head_dim are never copied: zero once
-        for (int i = tid; i < G::RING / 16; i += NT) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
-    }
     __syncthreads();
-    const int64_t total = (int64_t)s_pref[p.n_seq] * units;
-    int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    share = max((int64_t)p.min_tiles, (share + NW - 1) / NW * NW);
-    const int64_t x0 = share * blockIdx.x, x1 = min(total, x0 + share);
+    const unsigned total = (unsigned)s_pref[p.n_seq] * (unsigned)units, share = (total + gridDim.x - 1) / gridDim.x;    // below 2^31
+    const int x0 = (int)min(total, share * blockIdx.x), x1 = (int)min(total, x0 + share);
 
     const int nchunk = p.dim * G::EB / 16;
-    const int rows_cta = 8 * mt;
     const uint32_t my_ring = ring0 + (uint32_t)(warp * G::NST * G::STAGE);
+    const bool one_page = p.page_size % ATT_TILE == 0;           // a tile never leaves its page
+    const uint32_t k_row = ((lane >> 3) & 1) * 8 + (lane & 7), k_chunk = lane >> 4;       // ldmatrix addresses: K
+    const uint32_t v_row = TYPE == KV_Q8_0 ? k_row : (lane >> 4) * 8 + (lane & 7);        // and V
+    const uint32_t v_chunk = TYPE == KV_Q8_0 ? k_chunk : (lane >> 3) & 1;
 
-    for (int64_t x = x0; x < x1;) {
-        // ---- the segment: sequence, row block, head, and its tiles in this CTA
+    for (int x = x0; x < x1;) {
+        // ---- the segment: sequence, row block, head, and its steps in this CTA
         int s = 0;
         {
             int hi = p.n_seq;
             while (hi - s > 1) {
                 const int mid = (s + hi) >> 1;
-                if ((int64_t)s_pref[mid] * units <= x) s = mid;
+                if (s_pref[mid] * units <= x) s = mid;
                 else hi = mid;
             }
         }
         AttnSeq sq;
         sq.set(attn_len(p, s), p);
-        const int64_t seq0 = (int64_t)s_pref[s] * units;
-        const int unit = (int)((x - seq0) / sq.n_tiles);
-        const int rb = unit / p.n_kv, h = unit % p.n_kv;
-        const int64_t seg0 = seq0 + (int64_t)unit * sq.n_tiles, seg1 = seg0 + sq.n_tiles;
-        const int t0 = (int)(x - seg0), t1 = (int)(min(seg1, x1) - seg0);
-        const int row0 = rb * rows_cta;
-        const int n_steps = (t1 - t0 + NW - 1) / NW;
+        const int seq0 = s_pref[s] * units;
+        const int unit = (int)((unsigned)(x - seq0) / (unsigned)sq.n_steps);
+        const int rb = p.n_rb == 1 ? 0 : unit / p.n_kv, h = unit - rb * p.n_kv;
+        const int seg0 = seq0 + unit * sq.n_steps, seg1 = seg0 + sq.n_steps;
+        const int row0 = rb * G::ROWS;
+        const int tile0 = (x - seg0) * NW + warp;                         // this warp's first tile
+        const int k0 = x - seg0, k1 = min(seg1, x1) - seg0;               // steps of the segment
+        const int n_steps = max(0, min(k1, (sq.n_tiles - warp + NW - 1) / NW) - k0);      // this warp has a tile in
         const int32_t *tab = p.table + (int64_t)s * p.table_stride;
-        x += t1 - t0;
+        x += k1 - k0;
 
         // ---- the ring: page entries one step ahead of the copies
-        int pg_next = -1, slot_next = 0;
         auto fetch_page = [&](int step) {
-            const int tile = t0 + step * NW + warp;
-            pg_next = -1;
-            if (step < n_steps && tile < t1 && lane < ATT_TILE) {
-                const int j = sq.slot0(tile) + lane;
-                slot_next = j;
-                if (sq.seen(j)) {
-                    const int pi = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
-                    pg_next = __ldg(tab + pi);
-                    if (pg_next < 0 || pg_next >= p.n_pages) {
-                        atomicOr(p.err, 8 /* QMV_DEVERR_PAGE_ID */);
-                        pg_next = -1;
-                    }
+            int pg = -1;
+            if (step < n_steps) {
+                const int j = sq.slot0(tile0 + step * NW) + (one_page ? 0 : lane & (ATT_TILE - 1));
+                if (one_page ? j < sq.len : sq.seen(j)) {
+                    pg = __ldg(tab + (p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size));
                 }
             }
+            return pg;
         };
-        auto issue = [&](int step) {
-            const int tile = t0 + step * NW + warp;
-            if (step < n_steps && tile < t1) {
-                const int st = step % G::NST;
+        auto issue = [&](int step, int st, int pg) {
+            if (step < n_steps) {
                 const uint32_t dst = my_ring + (uint32_t)(st * G::STAGE);
-                const int o = p.page_shift >= 0 ? slot_next & (p.page_size - 1) : slot_next % p.page_size;
-                const long long e = pg_next < 0 ? -1
-                                                : pg_next * p.page_stride + h * p.head_stride + o * p.slot_stride;
-                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, pg_next >= 0);
-                if (lane == 0) s_mask[warp][st] = mask;
+                const int j0 = sq.slot0(tile0 + step * NW), j = j0 + (one_page ? 0 : lane & (ATT_TILE - 1));
+                const int o = p.page_shift >= 0 ? j & (p.page_size - 1) : j % p.page_size;
+                const long long e = pg * p.page_stride + h * p.head_stride + o * p.slot_stride;
+                const bool bad = pg < 0 || pg >= p.n_pages, want = lane < ATT_TILE && sq.seen(j0 + lane);
+                const uint32_t use = __ballot_sync(0xFFFFFFFFu, want && !bad);
+                if (want && bad) atomicOr(p.err, 8 /* QMV_DEVERR_PAGE_ID */);
+                if (lane == 0) s_mask[warp][st] = use;
                 constexpr int LPR = G::NCHUNK < 32 ? G::NCHUNK : 32;      // lanes of a row
                 constexpr int RPI = 32 / LPR;                             // rows of a pass
                 const int ch = lane % LPR;
+                // rows' addresses: from the tile's when it lies in one page, else from the lane of the row
+                const int64_t e1 = (e + (lane / LPR) * p.slot_stride) * G::EB + ch * 16, step_b = RPI * p.slot_stride * G::EB;
 #pragma unroll
-                for (int r0 = 0; r0 < ATT_TILE; r0 += RPI) {
-                    const int r = r0 + lane / LPR;
-                    const long long er = __shfl_sync(0xFFFFFFFFu, e, r);
-                    const uint32_t n = er >= 0 ? 16u : 0u;
-                    const int64_t at = er >= 0 ? er * G::EB + ch * 16 : 0;
-                    if (ch < nchunk) {
-                        cp_async16(dst + G::at(r, ch), p.k + at, n);
-                        cp_async16(dst + G::KV_BYTES + G::at(r, ch), p.v + at, n);
-                    }
+                for (int i = 0; i < ATT_TILE / RPI; ++i) {
+                    const int r = i * RPI + lane / LPR;
+                    const bool ok = ((use >> r) & 1u) && ch < nchunk;
+                    int64_t at = e1 + i * step_b;
+                    if (!one_page) at = __shfl_sync(0xFFFFFFFFu, e, r) * G::EB + ch * 16;
+                    if (!ok) at = 0;
+                    cp_async16(dst + G::at(r, ch), p.k + at, ok ? 16u : 0u);
+                    cp_async16(dst + G::KV_BYTES + G::at(r, ch), p.v + at, ok ? 16u : 0u);
                 }
-                if (TYPE == KV_Q8_0) {
+                if constexpr (TYPE == KV_Q8_0) {
                     constexpr int WPR = DP / 64;                          // 4-byte words of a slot's scales
                     const int nw = p.dim / 64;
 #pragma unroll
                     for (int i0 = 0; i0 < ATT_TILE * WPR; i0 += 32) {
                         const int r = (i0 + lane) / WPR, w = (i0 + lane) % WPR;
-                        const long long er = __shfl_sync(0xFFFFFFFFu, e, r & 15);
-                        const uint32_t n = er >= 0 ? 4u : 0u;
-                        const int64_t at = er >= 0 ? er / 16 + w * 4 : 0;
-                        if (r < ATT_TILE && w < nw) {
-                            cp_async4(dst + 2 * G::KV_BYTES + r * G::SC_PITCH + w * 4, p.ks + at, n);
-                            cp_async4(dst + 2 * G::KV_BYTES + G::SC_BYTES + r * G::SC_PITCH + w * 4, p.vs + at, n);
+                        const long long er = one_page ? e + r * p.slot_stride : __shfl_sync(0xFFFFFFFFu, e, r & 15);
+                        const bool ok = r < ATT_TILE && ((use >> r) & 1u) && w < nw;
+                        const int64_t at = ok ? er / 16 + w * 4 : 0;
+                        if (r < ATT_TILE) {
+                            cp_async4(dst + 2 * G::KV_BYTES + r * G::SC_PITCH + w * 4, p.ks + at, ok ? 4u : 0u);
+                            cp_async4(dst + 2 * G::KV_BYTES + G::SC_BYTES + r * G::SC_PITCH + w * 4, p.vs + at, ok ? 4u : 0u);
                         }
                     }
                 }
             }
             cp_commit();
         };
-        fetch_page(0);
+        int pg_next;
+        {
+            int pg[G::NST];
 #pragma unroll
-        for (int i = 0; i < G::NST - 1; ++i) {
-            issue(i);
-            fetch_page(i + 1);
+            for (int i = 0; i < G::NST; ++i) pg[i] = fetch_page(i);
+#pragma unroll
+            for (int i = 0; i < G::NST - 1; ++i) issue(i, i, pg[i]);
+            pg_next = pg[G::NST - 1];
         }
 
-        // ---- q as operand fragments: thread (g, c4) holds its row's values at
-        // columns 2 c4, 2 c4 + 1 and + 8 of every 16 (Q8_0: 4 c4 .. 4 c4 + 3, the
-        // order in which its k bytes come)
-        uint32_t aq[G::QREG ? DP / 16 : 1][G::QS_WORDS];
-        const int row = row0 + mi * 8 + g;
-        const bool row_ok = row < p.rows;
-        const int tok = row_ok ? row / p.group : 0;
-        const int at = sq.first + tok;                                    // the query's slot
-        float sfac = p.scale_log2;
-        {
-            const float *qr = p.q + (int64_t)(s * p.n_tok + tok) * p.q_stride + (int64_t)(h * p.group + (row_ok ? row % p.group : 0)) * p.dim;
+        // ---- q as B fragments: lane (g, c4) holds row g's values at columns
+        // 2 c4, 2 c4 + 1 and + 8 of every 16 (Q8_0: 4 c4 .. 4 c4 + 3, the order in
+        // which its k bytes come).  In registers for 8 narrow rows, else in shared memory.
+        uint32_t qr[G::QREG ? DP / 16 : 1][QW];
+        const uint32_t qs0 = ring0 + G::RING;
+        auto q_block = [&](int nb, auto &&put) {                          // returns the row's factor of the scores
+            const int row = row0 + nb * 8 + g;
+            const bool row_ok = row < p.rows;
+            const int tok = row_ok ? row / p.group : 0;
+            const float *x = p.q + (int64_t)(s * p.n_tok + tok) * p.q_stride + (int64_t)(h * p.group + (row_ok ? row - tok * p.group : 0)) * p.dim;
             auto load4 = [&](int ks, float (&f)[4]) {
                 const int d0 = ks * 16 + (TYPE == KV_Q8_0 ? 4 * c4 : 2 * c4), d1 = TYPE == KV_Q8_0 ? d0 + 2 : d0 + 8;
                 const bool ok = row_ok && ks * 16 < p.dim;
-                const float2 a = ok ? __ldg(reinterpret_cast<const float2 *>(qr + d0)) : make_float2(0.f, 0.f);
-                const float2 b = ok ? __ldg(reinterpret_cast<const float2 *>(qr + d1)) : make_float2(0.f, 0.f);
+                const float2 a = ok ? __ldg(reinterpret_cast<const float2 *>(x + d0)) : make_float2(0.f, 0.f);
+                const float2 b = ok ? __ldg(reinterpret_cast<const float2 *>(x + d1)) : make_float2(0.f, 0.f);
                 f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
             };
-            float qmul = 1.f;
-            if (TYPE != KV_BF16) {
+            float qmul = 1.f, sf = p.scale_log2;
+            if constexpr (TYPE != KV_BF16) {
                 float mx = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
@@ -410,220 +456,307 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP>::THREADS, 1) attn_decode_ke
                 const int ex = (int)(__float_as_uint(mx) >> 23) - 127;
                 const int sh = mx > 0.f ? min(100, 12 - ex) : 0;
                 qmul = __uint_as_float((uint32_t)(127 + sh) << 23);
-                sfac *= __uint_as_float((uint32_t)(127 - sh) << 23);
+                sf *= __uint_as_float((uint32_t)(127 - sh) << 23);
             }
-            uint32_t *qs = reinterpret_cast<uint32_t *>(smem + G::RING) + (size_t)mi * (DP / 16) * 32 * G::QS_WORDS;
-            if (!G::QREG) __syncthreads();                                // the last segment's reads of it are done
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ++ks) {
                 float f[4];
                 load4(ks, f);
-                uint32_t w[G::QS_WORDS];
+                uint32_t w[QW];
                 if constexpr (TYPE == KV_BF16) {
-                    split_bf16(f[0], f[1], w[0], w[1], w[4]);
-                    split_bf16(f[2], f[3], w[2], w[3], w[5]);
+                    split_bf16(f[0], f[1], w[0], w[2], w[4]);
+                    split_bf16(f[2], f[3], w[1], w[3], w[5]);
                 } else {
-                    split_f16(f[0] * qmul, f[1] * qmul, w[0], w[1]);
-                    split_f16(f[2] * qmul, f[3] * qmul, w[2], w[3]);
+                    split_f16(f[0] * qmul, f[1] * qmul, w[0], w[2]);
+                    split_f16(f[2] * qmul, f[3] * qmul, w[1], w[3]);
                 }
-                if (G::QREG) {
-#pragma unroll
-                    for (int i = 0; i < G::QS_WORDS; ++i) aq[G::QREG ? ks : 0][i] = w[i];
-                } else if (kg == 0) {
-#pragma unroll
-                    for (int i = 0; i < G::QS_WORDS; ++i) qs[(ks * G::QS_WORDS + i) * 32 + lane] = w[i];
-                }
+                put(ks, w);
             }
-            if (!G::QREG) __syncthreads();
+            return sf;
+        };
+        for (int r = tid; r < G::ROWS; r += NT) s_at[r] = row0 + r < p.rows ? sq.first + (row0 + r) / p.group : -1;
+        float sf[MB][2];                                                  // of rows 2 c4, 2 c4 + 1 of every block
+        if constexpr (G::QREG) {
+            const float f = q_block(0, [&](int ks, const uint32_t (&w)[QW]) {
+#pragma unroll
+                for (int i = 0; i < QW; ++i) qr[ks][i] = w[i];
+            });
+            sf[0][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * c4);
+            sf[0][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * c4 + 4);
+            __syncthreads();
+        } else {
+            for (int nb = warp; nb < MB; nb += NW) {
+                const float f = q_block(nb, [&](int ks, const uint32_t (&w)[QW]) {
+                    const uint32_t a = qs0 + (uint32_t)((nb * (DP / 16) + ks) * 32 * QW * 4);
+                    sts_v4(a + lane * 16, make_uint4(w[0], w[1], w[2], w[3]));
+                    if constexpr (QW == 6) sts_v2(a + 512 + lane * 8, make_uint2(w[4], w[5]));
+                });
+                if (c4 == 0) s_sf[nb * 8 + g] = f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int nb = 0; nb < MB; ++nb) {
+                sf[nb][0] = s_sf[nb * 8 + 2 * c4];
+                sf[nb][1] = s_sf[nb * 8 + 2 * c4 + 1];
+            }
         }
-        auto q_frag = [&](int ks, uint32_t (&w)[G::QS_WORDS]) {
-            if (G::QREG) {
+        auto q_frag = [&](int nb, int ks, uint32_t (&w)[QW]) {
+            if constexpr (G::QREG) {
 #pragma unroll
-                for (int i = 0; i < G::QS_WORDS; ++i) w[i] = aq[G::QREG ? ks : 0][i];
+                for (int i = 0; i < QW; ++i) w[i] = qr[ks][i];
             } else {
-                const uint32_t a = ring0 + G::RING + (uint32_t)((mi * (DP / 16) + ks) * G::QS_WORDS * 32 + lane) * 4u;
-#pragma unroll
-                for (int i = 0; i < G::QS_WORDS; ++i) w[i] = lds_u32(a + (uint32_t)i * 128u);
+                const uint32_t a = qs0 + (uint32_t)((nb * (DP / 16) + ks) * 32 * QW * 4);
+                const uint4 u = lds_v4(a + lane * 16);
+                w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+                if constexpr (QW == 6) {
+                    const uint2 v = lds_v2(a + 512 + lane * 8);
+                    w[4] = v.x; w[5] = v.y;
+                }
             }
         };
 
-        float m = -INFINITY, l = 0.f;
-        float o[DP / 8][4];
+        float m[MB][2], l[MB][2], acc[MB][DP / 16][4];
 #pragma unroll
-        for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float *raw = p.score ? p.raw + ((int64_t)(s * p.n_kv + h) * p.rows + row) * p.raw_stride : nullptr;
+        for (int nb = 0; nb < MB; ++nb) {
+            m[nb][0] = m[nb][1] = -INFINITY;
+            l[nb][0] = l[nb][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.f;
+        }
 
+        int st = 0;
         for (int step = 0; step < n_steps; ++step) {
             cp_wait<G::NST - 2>();
-            if (mt == 1) __syncwarp();
-            else named_bar_sync(1 + kg, 32 * mt);
-            issue(step + G::NST - 1);
-            fetch_page(step + G::NST);
-            const int st = step % G::NST;
-            for (int mm = 0; mm < mt; ++mm) {
-                const int w = kg * mt + mm, tile = t0 + step * NW + w;
-                if (tile >= t1) break;
-                const uint32_t buf = ring0 + (uint32_t)((w * G::NST + st) * G::STAGE);
-                const int j0 = sq.slot0(tile);
-                const uint32_t use = s_mask[w][st];
-                // -- scores of 16 slots: this thread's are slots 2 c4, 2 c4 + 1 and + 8
-                float sc[2][4] = {};
-                const uint32_t kaddr_r = (uint32_t)((lane >> 4) * 8 + (lane & 7)), kaddr_c = (uint32_t)((lane >> 3) & 1);
-                if constexpr (TYPE == KV_Q8_0) {
+            __syncwarp();
+            issue(step + G::NST - 1, st == 0 ? G::NST - 1 : st - 1, pg_next);
+            pg_next = fetch_page(step + G::NST);
+            const int j0 = sq.slot0(tile0 + step * NW);
+            const uint32_t buf = my_ring + (uint32_t)(st * G::STAGE), use = s_mask[warp][st];
+            if (++st == G::NST) st = 0;
+            // -- scores: this lane's are slots g (values 0, 1) and g + 8 (2, 3), rows 2 c4 and 2 c4 + 1 of every block
+            float sc[MB][4];
+            if constexpr (TYPE == KV_Q8_0) {
 #pragma unroll
-                    for (int b = 0; b < DP / 32; ++b) {
-                        uint32_t r[4];
-                        ldsm4(r, buf + G::at(kaddr_r, 2 * b + kaddr_c));
-                        float a[2][4] = {};
+                for (int nb = 0; nb < MB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+#pragma unroll
+                for (int b = 0; b < DP / 32; ++b) {
+                    uint32_t r[4], a[2][4];
+                    ldsm4(r, buf + G::at(k_row, 2 * b + k_chunk));
+#pragma unroll
+                    for (int k2 = 0; k2 < 2; ++k2) {
+                        i8_to_f16(r[2 * k2], a[k2][0], a[k2][2]);
+                        i8_to_f16(r[2 * k2 + 1], a[k2][1], a[k2][3]);
+                    }
+                    const uint32_t sa = buf + 2 * G::KV_BYTES + 2 * b;
+                    const float d0 = half_bits_to_float(lds_u16(sa + g * G::SC_PITCH)), d1 = half_bits_to_float(lds_u16(sa + (g + 8) * G::SC_PITCH));
+#pragma unroll
+                    for (int nb = 0; nb < MB; ++nb) {
+                        float hi[4] = {}, lo[4] = {};
 #pragma unroll
                         for (int k2 = 0; k2 < 2; ++k2) {
-                            uint32_t q[G::QS_WORDS];
-                            q_frag(2 * b + k2, q);
-#pragma unroll
-                            for (int nt = 0; nt < 2; ++nt) {
-                                uint32_t b0, b1;
-                                i8_to_f16(r[2 * nt + k2], b0, b1);
-                                mma_f16(a[nt], q[0], q[1], q[2], q[3], b0, b1);
-                            }
+                            uint32_t q[QW];
+                            q_frag(nb, 2 * b + k2, q);
+                            mma_16<false>(hi, a[k2], q[0], q[1]);
+                            mma_16<false>(lo, a[k2], q[2], q[3]);
                         }
-#pragma unroll
-                        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const float d = half_bits_to_float(lds_u16(buf + 2 * G::KV_BYTES + (uint32_t)((nt * 8 + 2 * c4 + i) * G::SC_PITCH + 2 * b)));
-                                sc[nt][i] = fmaf(d, a[nt][i] + a[nt][i + 2], sc[nt][i]);
-                            }
-                    }
-                } else {
-#pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks) {
-                        uint32_t r[4], q[G::QS_WORDS];
-                        ldsm4(r, buf + G::at(kaddr_r, 2 * ks + kaddr_c));
-                        q_frag(ks, q);
-#pragma unroll
-                        for (int nt = 0; nt < 2; ++nt) {
-                            if constexpr (TYPE == KV_F16) {
-                                mma_f16(sc[nt], q[0], q[1], q[2], q[3], r[2 * nt], r[2 * nt + 1]);
-                            } else {
-                                mma_bf16(sc[nt], q[0], q[1], q[2], q[3], r[2 * nt], r[2 * nt + 1]);
-                                mma_bf16(sc[nt], q[4], 0u, q[5], 0u, r[2 * nt], r[2 * nt + 1]);
-                            }
-                        }
+                        sc[nb][0] = fmaf(d0, hi[0] + lo[0], sc[nb][0]);
+                        sc[nb][1] = fmaf(d0, hi[1] + lo[1], sc[nb][1]);
+                        sc[nb][2] = fmaf(d1, hi[2] + lo[2], sc[nb][2]);
+                        sc[nb][3] = fmaf(d1, hi[3] + lo[3], sc[nb][3]);
                     }
                 }
-                float sv[4];
-                bool vis[4];
+            } else {
+                constexpr int PAR = MB == 1 ? 2 : 1;                      // chains per part: their sums wait on the one before
+                float a[MB][NPQ][PAR][4] = {};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int jj = (i >> 1) * 8 + 2 * c4 + (i & 1);
-                    const float t = TYPE == KV_Q8_0 ? sc[i >> 1][i & 1] : sc[i >> 1][i & 1] + sc[i >> 1][(i & 1) + 2];
-                    vis[i] = row_ok && ((use >> jj) & 1u) && attn_sees(p, at, j0 + jj);
-                    sv[i] = vis[i] ? t * sfac : -INFINITY;
-                }
-                if (raw && row_ok) {
-                    *reinterpret_cast<float2 *>(raw + j0 + 2 * c4) = make_float2(sv[0], sv[1]);
-                    *reinterpret_cast<float2 *>(raw + j0 + 8 + 2 * c4) = make_float2(sv[2], sv[3]);
-                }
-                // -- the running maximum and sum
-                float mx = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-                const float mn = fmaxf(m, mx);
-                if (__any_sync(0xFFFFFFFFu, mn > m)) {
-                    const float f = m == mn ? 1.f : exp2f(m - mn);        // m = -inf: 0
-                    l *= f;
+                for (int ks = 0; ks < DP / 16; ++ks) {
+                    uint32_t r[4];
+                    ldsm4(r, buf + G::at(k_row, 2 * ks + k_chunk));
 #pragma unroll
-                    for (int i = 0; i < DP / 8; ++i) {
-                        o[i][0] *= f; o[i][1] *= f; o[i][2] *= f; o[i][3] *= f;
+                    for (int nb = 0; nb < MB; ++nb) {
+                        uint32_t q[QW];
+                        q_frag(nb, ks, q);
+#pragma unroll
+                        for (int i = 0; i < NPQ; ++i) mma_16<TYPE == KV_BF16>(a[nb][i][ks % PAR], r, q[2 * i], q[2 * i + 1]);
                     }
-                    m = mn;
                 }
-                // f16 parts: weights times 2^15, so that their low parts stay normal
-                const float mref = (m == -INFINITY ? 0.f : m) - p.l_shift;
-                float pr[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    pr[i] = exp2f(sv[i] - mref);
-                    l += pr[i];
+                for (int nb = 0; nb < MB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float t = 0.f;
+#pragma unroll
+                        for (int i = NPQ - 1; i >= 0; --i) t += PAR == 2 ? a[nb][i][0][e] + a[nb][i][PAR - 1][e] : a[nb][i][0][e];
+                        sc[nb][e] = t;
+                    }
+            }
+#pragma unroll
+            for (int nb = 0; nb < MB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nb][e] *= sf[nb][e & 1];
+            const bool mixed = p.n_tok > 1 && (use != 0xFFFFu || !sq.by_all(j0, p));
+            if (mixed) {
+#pragma unroll
+                for (int nb = 0; nb < MB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int jj = g + (e >> 1) * 8;
+                        if (!((use >> jj) & 1u) || !attn_sees(p, s_at[nb * 8 + 2 * c4 + (e & 1)], j0 + jj)) sc[nb][e] = -INFINITY;
+                    }
+            } else if (use != 0xFFFFu) {                                  // one query: what it sees was loaded
+                const bool u0 = (use >> g) & 1u, u1 = (use >> (g + 8)) & 1u;
+#pragma unroll
+                for (int nb = 0; nb < MB; ++nb) {
+                    if (!u0) sc[nb][0] = sc[nb][1] = -INFINITY;
+                    if (!u1) sc[nb][2] = sc[nb][3] = -INFINITY;
                 }
-                // -- output += weights x values
-                const uint32_t va = buf + G::KV_BYTES;
-                const uint32_t vaddr_r = (uint32_t)(((lane >> 3) & 1) * 8 + (lane & 7)), vaddr_c = (uint32_t)(lane >> 4);
-                if constexpr (TYPE == KV_Q8_0) {
+            }
+            if (p.score) {
+                float *raw = p.raw + ((int64_t)(s * p.n_kv + h) * p.raw_stride + j0 + g) * p.raw_rows + row0 + 2 * c4;
 #pragma unroll
-                    for (int b = 0; b < DP / 32; ++b) {
-                        uint32_t r[4], a[6];
-                        ldsm4t(r, va + G::at(vaddr_r, 2 * b + vaddr_c));
+                for (int nb = 0; nb < MB; ++nb)
+                    if (row0 + nb * 8 + 2 * c4 < p.raw_rows) {
+                        *reinterpret_cast<float2 *>(raw + nb * 8) = make_float2(sc[nb][0], sc[nb][1]);
+                        *reinterpret_cast<float2 *>(raw + nb * 8 + 8 * (int64_t)p.raw_rows) = make_float2(sc[nb][2], sc[nb][3]);
+                    }
+            }
+            // -- the running maximum: moved only when a score is well above it
+            bool up = false;
+#pragma unroll
+            for (int nb = 0; nb < MB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) up |= fmaxf(sc[nb][e], sc[nb][e + 2]) > m[nb][e] + attn_slack(TYPE);
+            if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+                for (int nb = 0; nb < MB; ++nb) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(sc[nb][e], sc[nb][e + 2]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+                        const float mn = fmaxf(m[nb][e], mx);
+                        f[e] = m[nb][e] == mn ? 1.f : ex2(m[nb][e] - mn);         // m = -inf: 0
+                        m[nb][e] = mn;
+                        l[nb][e] *= f[e];
+                    }
+#pragma unroll
+                    for (int i = 0; i < DP / 16; ++i) {
+                        mul2(acc[nb][i][0], acc[nb][i][1], f[0], f[1]);
+                        mul2(acc[nb][i][2], acc[nb][i][3], f[0], f[1]);
+                    }
+                }
+            }
+            // -- the weights
+#pragma unroll
+            for (int nb = 0; nb < MB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mref = (m[nb][e] == -INFINITY ? 0.f : m[nb][e]) - p.l_shift;
+                    sc[nb][e] = ex2(sc[nb][e] - mref);
+                    sc[nb][e + 2] = ex2(sc[nb][e + 2] - mref);
+                    l[nb][e] += sc[nb][e] + sc[nb][e + 2];
+                }
+            // -- output += values x weights
+            const uint32_t va = buf + G::KV_BYTES;
+            if constexpr (TYPE == KV_Q8_0) {
+                // weights transposed to lane (row g, slots 2 c4, 2 c4 + 1 and + 8) as halves of 16 bits, then scaled per block of 32
+                float pw[MB][4];
+#pragma unroll
+                for (int nb = 0; nb < MB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t u0 = __float_as_uint(sc[nb][2 * i]), u1 = __float_as_uint(sc[nb][2 * i + 1]);
+                        const uint32_t hi = movm_t(__byte_perm(u0, u1, 0x7632)), lo = movm_t(__byte_perm(u0, u1, 0x5410));
+                        pw[nb][2 * i] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
+                        pw[nb][2 * i + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+                    }
+#pragma unroll
+                for (int b = 0; b < DP / 32; ++b) {
+                    uint32_t r[4];
+                    ldsm4t(r, va + G::at(v_row, 2 * b + v_chunk));
+                    const uint32_t sa = buf + 2 * G::KV_BYTES + G::SC_BYTES + 2 * b;
+                    float d[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        d[i] = half_bits_to_float(lds_u16(sa + (2 * c4 + (i & 1) + (i >> 1) * 8) * G::SC_PITCH));
+                        if (mixed && !(fabsf(d[i]) < INFINITY)) d[i] = 0.f;       // NaN of a slot that this row may not see: its weight is 0
+                    }
+                    uint32_t a[2][4];
+#pragma unroll
+                    for (int k2 = 0; k2 < 2; ++k2) {                      // rows g and g + 8: dims 2 g and 2 g + 1 of 16
+                        i8_to_bf16(r[2 * k2], a[k2][0], a[k2][1]);
+                        i8_to_bf16(r[2 * k2 + 1], a[k2][2], a[k2][3]);
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < MB; ++nb) {
                         float pd[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int jj = (i >> 1) * 8 + 2 * c4 + (i & 1);
-                            const float d = half_bits_to_float(lds_u16(buf + 2 * G::KV_BYTES + G::SC_BYTES + (uint32_t)(jj * G::SC_PITCH + 2 * b)));
-                            pd[i] = vis[i] ? pr[i] * d : 0.f;
-                        }
-                        split_bf16(pd[0], pd[1], a[0], a[1], a[4]);
-                        split_bf16(pd[2], pd[3], a[2], a[3], a[5]);
+                        for (int i = 0; i < 4; ++i) pd[i] = pw[nb][i] * d[i];
+                        uint32_t pb[3][2];
+                        split_bf16(pd[0], pd[1], pb[0][0], pb[1][0], pb[2][0]);
+                        split_bf16(pd[2], pd[3], pb[0][1], pb[1][1], pb[2][1]);
 #pragma unroll
                         for (int k2 = 0; k2 < 2; ++k2) {
-                            uint32_t e0, e1, d0, d1;                       // even and odd columns of 16
-                            i8_to_bf16(r[2 * k2], e0, d0);
-                            i8_to_bf16(r[2 * k2 + 1], e1, d1);
-                            mma_bf16(o[4 * b + 2 * k2], a[0], a[1], a[2], a[3], e0, e1);
-                            mma_bf16(o[4 * b + 2 * k2], a[4], 0u, a[5], 0u, e0, e1);
-                            mma_bf16(o[4 * b + 2 * k2 + 1], a[0], a[1], a[2], a[3], d0, d1);
-                            mma_bf16(o[4 * b + 2 * k2 + 1], a[4], 0u, a[5], 0u, d0, d1);
+                            float t[4] = {};
+#pragma unroll
+                            for (int i = 2; i >= 0; --i) mma_16<true>(t, a[k2], pb[i][0], pb[i][1]);
+                            add2(acc[nb][2 * b + k2][0], acc[nb][2 * b + k2][1], t[0], t[1]);
+                            add2(acc[nb][2 * b + k2][2], acc[nb][2 * b + k2][3], t[2], t[3]);
+                        }
+                    }
+                }
+            } else {
+                uint32_t pb[MB][NPP][2];
+#pragma unroll
+                for (int nb = 0; nb < MB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t w[3];
+                        if constexpr (TYPE == KV_F16) split_f16(sc[nb][2 * i], sc[nb][2 * i + 1], w[0], w[1]);
+                        else split_bf16(sc[nb][2 * i], sc[nb][2 * i + 1], w[0], w[1], w[2]);
+#pragma unroll
+                        for (int k = 0; k < NPP; ++k) pb[nb][k][i] = movm_t(w[k]);
+                    }
+                if (!mixed) {
+#pragma unroll
+                    for (int i = 0; i < DP / 16; ++i) {
+                        uint32_t r[4];
+                        ldsm4t(r, va + G::at(v_row, 2 * i + v_chunk));
+#pragma unroll
+                        for (int nb = 0; nb < MB; ++nb) {
+                            float t[4] = {};
+#pragma unroll
+                            for (int k = NPP - 1; k >= 0; --k) mma_16<PBF>(t, r, pb[nb][k][0], pb[nb][k][1]);
+                            add2(acc[nb][i][0], acc[nb][i][1], t[0], t[1]);
+                            add2(acc[nb][i][2], acc[nb][i][3], t[2], t[3]);
                         }
                     }
                 } else {
-                    uint32_t a[6];
-                    if constexpr (TYPE == KV_F16) {
-                        split_f16(pr[0], pr[1], a[0], a[1]);
-                        split_f16(pr[2], pr[3], a[2], a[3]);
-                    } else {
-                        split_bf16(pr[0], pr[1], a[0], a[1], a[4]);
-                        split_bf16(pr[2], pr[3], a[2], a[3], a[5]);
-                    }
-                    auto pv = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
-                        if constexpr (TYPE == KV_F16) {
-                            mma_f16(acc, a[0], a[1], a[2], a[3], b0, b1);
-                        } else {
-                            mma_bf16(acc, a[0], a[1], a[2], a[3], b0, b1);
-                            mma_bf16(acc, a[4], 0u, a[5], 0u, b0, b1);
+                    // query by query, the values it does not see as zeros
+                    const int tk1 = (min(row0 + G::ROWS, p.rows) - 1) / p.group;
+                    for (int tk = row0 / p.group; tk <= tk1; ++tk) {
+                        const int at = sq.first + tk;
+                        uint32_t z[2];                                    // of slots 2 c4, 2 c4 + 1 and + 8
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int j = j0 + 8 * i + 2 * c4;
+                            z[i] = (attn_sees(p, at, j) ? 0xFFFFu : 0u) | (attn_sees(p, at, j + 1) ? 0xFFFF0000u : 0u);
                         }
-                    };
-                    const bool mixed = p.n_tok > 1 && tile >= sq.sink_tiles &&
-                                       (j0 + ATT_TILE - 1 > sq.first || (p.window > 0 && j0 <= sq.len - 1 - p.window));
-                    if (!mixed) {
 #pragma unroll
                         for (int i = 0; i < DP / 16; ++i) {
                             uint32_t r[4];
-                            ldsm4t(r, va + G::at(vaddr_r, 2 * i + vaddr_c));
-                            pv(o[2 * i], r[0], r[1]);
-                            pv(o[2 * i + 1], r[2], r[3]);
-                        }
-                    } else {
-                        // token by token, the values it does not see as zeros
-                        const int tk0 = (row0 + mi * 8) / p.group, tk1 = min(row0 + mi * 8 + 7, p.rows - 1) / p.group;
-                        for (int tk = tk0; tk <= tk1; ++tk) {
-                            uint32_t z[2];
+                            ldsm4t(r, va + G::at(v_row, 2 * i + v_chunk));
+                            r[0] &= z[0]; r[1] &= z[0]; r[2] &= z[1]; r[3] &= z[1];
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int j = j0 + 8 * i + 2 * c4;
-                                z[i] = (attn_sees(p, sq.first + tk, j) ? 0xFFFFu : 0u) | (attn_sees(p, sq.first + tk, j + 1) ? 0xFFFF0000u : 0u);
-                            }
+                            for (int nb = 0; nb < MB; ++nb) {
+                                float t[4] = {};
 #pragma unroll
-                            for (int i = 0; i < DP / 16; ++i) {
-                                uint32_t r[4];
-                                ldsm4t(r, va + G::at(vaddr_r, 2 * i + vaddr_c));
+                                for (int k = NPP - 1; k >= 0; --k) mma_16<PBF>(t, r, pb[nb][k][0], pb[nb][k][1]);
 #pragma unroll
-                                for (int n2 = 0; n2 < 2; ++n2) {
-                                    float acc[4] = {};
-                                    pv(acc, r[2 * n2] & z[0], r[2 * n2 + 1] & z[1]);
-                                    if (tk == tok) {
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) o[2 * i + n2][e] += acc[e];
-                                    }
-                                }
+                                for (int e = 0; e < 4; ++e)
+                                    if (s_at[nb * 8 + 2 * c4 + (e & 1)] == at) acc[nb][i][e] += t[e];
                             }
                         }
                     }
@@ -631,152 +764,204 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP>::THREADS, 1) attn_decode_ke
             }
         }
         cp_wait<0>();
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-        if (c4 == 0) {
-            s_m[warp][g] = m;
-            s_l[warp][g] = l;
-        }
-        __syncthreads();                                                  // the ring is free
-
-        // ---- join the key groups' parts (in the ring)
-        float *so = reinterpret_cast<float *>(smem);
-        {
-            float mr = -INFINITY;
-            for (int w = mi; w < NW / mt * mt; w += mt) mr = fmaxf(mr, s_m[w][g]);
-            const float f = m == mr ? 1.f : exp2f(m - mr);
-            float *ow = so + (size_t)(warp * 8 + g) * G::OPITCH;
 #pragma unroll
-            for (int i = 0; i < DP / 16; ++i) {
-                const float v0 = (o[2 * i][0] + o[2 * i][2]) * f, v1 = (o[2 * i][1] + o[2 * i][3]) * f;
-                const float u0 = (o[2 * i + 1][0] + o[2 * i + 1][2]) * f, u1 = (o[2 * i + 1][1] + o[2 * i + 1][3]) * f;
-                if (TYPE == KV_Q8_0) {
-                    *reinterpret_cast<float4 *>(ow + 16 * i + 4 * c4) = make_float4(v0, u0, v1, u1);
-                } else {
-                    *reinterpret_cast<float2 *>(ow + 16 * i + 2 * c4) = make_float2(v0, v1);
-                    *reinterpret_cast<float2 *>(ow + 16 * i + 8 + 2 * c4) = make_float2(u0, u1);
+        for (int nb = 0; nb < MB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float t = l[nb][e];
+                t += __shfl_xor_sync(0xFFFFFFFFu, t, 4);
+                t += __shfl_xor_sync(0xFFFFFFFFu, t, 8);
+                t += __shfl_xor_sync(0xFFFFFFFFu, t, 16);
+                if (g == 0) {
+                    s_m[warp][nb * 8 + 2 * c4 + e] = m[nb][e];
+                    s_l[warp][nb * 8 + 2 * c4 + e] = t;
                 }
             }
-            if (kg == 0 && c4 == 0) {
-                float lr = 0.f;
-                for (int w = mi; w < NW; w += mt) lr += s_m[w][g] == mr ? s_l[w][g] : s_l[w][g] * exp2f(s_m[w][g] - mr);
-                s_mr[mi * 8 + g] = mr;
-                s_lr[mi * 8 + g] = lr;
+        __syncthreads();                                                  // the ring is free
+
+        // ---- join the warps' parts (in the ring); one without a tile has m = -inf, l = 0, o = 0
+        float *so = reinterpret_cast<float *>(smem);
+#pragma unroll
+        for (int nb = 0; nb < MB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = nb * 8 + 2 * c4 + e;
+                float mr = s_m[0][r];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) mr = fmaxf(mr, s_m[w][r]);
+                const float f = m[nb][e] == mr ? 1.f : ex2(m[nb][e] - mr);
+                float *ow = so + (size_t)(warp * G::ROWS + r) * G::OPITCH;
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    const float v0 = acc[nb][i][e] * f, v1 = acc[nb][i][e + 2] * f;
+                    if constexpr (TYPE == KV_Q8_0) {
+                        *reinterpret_cast<float2 *>(ow + 16 * i + 2 * g) = make_float2(v0, v1);
+                    } else {
+                        ow[16 * i + g] = v0;
+                        ow[16 * i + 8 + g] = v1;
+                    }
+                }
             }
-        }
-        __syncthreads();
-        const int nrow = min(rows_cta, p.rows - row0);
-        auto put = [&](int r, int d, float v) {
-            const int rr = row0 + r, t = rr / p.group, hq = rr % p.group;
-            p.out[(int64_t)(s * p.n_tok + t) * p.out_stride + (int64_t)(h * p.group + hq) * p.dim + d] = v;
+        const int nrow = min(G::ROWS, p.rows - row0);
+        auto out_row = [&](int r) {
+            const int t = s_at[r] - sq.first;
+            return p.out + (int64_t)(s * p.n_tok + t) * p.out_stride + (int64_t)(h * p.group + row0 + r - t * p.group) * p.dim;
         };
         auto put_stats = [&](int r, float mr, float lr) {
-            if (p.score) {
-                float *q = p.stats + 2 * ((int64_t)(s * p.n_kv + h) * p.rows + row0 + r);
-                q[0] = mr;
-                q[1] = lr;
-            }
+            if (p.score) *reinterpret_cast<float2 *>(p.stats + 2 * ((int64_t)(s * p.n_kv + h) * p.rows + row0 + r)) = make_float2(mr, lr);
         };
         const bool whole = seg0 >= x0 && seg1 <= x1;
         const int slot = 2 * blockIdx.x + (seg0 >= x0 ? 1 : 0);
-        for (int i = tid; i < nrow * p.dim; i += NT) {
-            const int r = i / p.dim, d = i % p.dim;
-            float v = 0.f;
-            for (int k2 = 0; k2 < NW / mt; ++k2) v += so[(size_t)((k2 * mt + (r >> 3)) * 8 + (r & 7)) * G::OPITCH + d];
-            if (whole) put(r, d, s_lr[r] != 0.f ? v / s_lr[r] : 0.f);
-            else p.part_o[((int64_t)slot * rows_cta + r) * p.dim + d] = v;
-        }
         if (tid < nrow) {
-            if (whole) {
-                put_stats(tid, s_mr[tid], s_lr[tid]);
-            } else {
-                float *q = p.part_ml + 2 * ((int64_t)slot * rows_cta + tid);
-                q[0] = s_mr[tid];
-                q[1] = s_lr[tid];
+            float mr = s_m[0][tid], lr = 0.f;
+#pragma unroll
+            for (int w = 1; w < NW; ++w) mr = fmaxf(mr, s_m[w][tid]);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) lr += s_m[w][tid] == mr ? s_l[w][tid] : s_l[w][tid] * ex2(s_m[w][tid] - mr);
+            s_lr[tid] = lr;
+            if (whole) put_stats(tid, mr, lr);
+            else __stcg(reinterpret_cast<float2 *>(p.part_ml) + (int64_t)slot * G::ROWS + tid, make_float2(mr, lr));
+        }
+        __syncthreads();
+        constexpr int D4 = DP / 4;                                        // a thread takes 4 dims of a row
+        auto put = [&](int r, int d, float4 v, float lr) {
+            float *o = out_row(r) + 4 * d;
+            o[0] = lr != 0.f ? v.x / lr : 0.f;
+            o[1] = lr != 0.f ? v.y / lr : 0.f;
+            o[2] = lr != 0.f ? v.z / lr : 0.f;
+            o[3] = lr != 0.f ? v.w / lr : 0.f;
+        };
+        for (int i = tid; i < nrow * D4; i += NT) {
+            const int r = i / D4, d = i % D4;
+            if (4 * d >= p.dim) continue;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float4 u = *reinterpret_cast<const float4 *>(so + (size_t)(w * G::ROWS + r) * G::OPITCH + 4 * d);
+                v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
             }
+            if (whole) put(r, d, v, s_lr[r]);
+            else __stcg(reinterpret_cast<float4 *>(p.part_o + ((int64_t)slot * G::ROWS + r) * p.dim) + d, v);
         }
         if (!whole) {
             // ---- the last CTA of the segment joins its parts, in CTA order
-            const int cta0 = (int)(seg0 / share), cta1 = (int)((seg1 - 1) / share), n = cta1 - cta0 + 1;
-            __threadfence();
+            const int cta0 = (int)((unsigned)seg0 / share), cta1 = (int)((unsigned)(seg1 - 1) / share), n = cta1 - cta0 + 1;
             __syncthreads();
             if (tid == 0) {
-                const unsigned done = atomicAdd(p.counters + cta0, 1u);
-                s_last = done == (unsigned)(n - 1);
-                if (s_last) p.counters[cta0] = 0u;
+                __threadfence();
+                s_last = atomicAdd(p.counters + cta0, 1u) == (unsigned)(n - 1);
+                __threadfence();
             }
             __syncthreads();
             if (s_last) {
-                __threadfence();
-                auto slot_of = [&](int i) { return 2 * (cta0 + i) + (i == 0 ? 1 : 0); };
-                float *fac = reinterpret_cast<float *>(smem);             // [n][nrow]
-                for (int r = warp; r < nrow; r += NW) {
+                if (tid == 0) p.counters[cta0] = 0u;
+                constexpr int CH = 8;                                     // parts in flight
+                for (int i = tid; i < nrow * D4; i += NT) {
+                    const int r = i / D4, d = i % D4;
+                    if (4 * d >= p.dim) continue;
+                    // part c: the second of CTA cta0's two slots for c = 0, else the first of CTA cta0 + c's
+                    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + (int64_t)2 * cta0 * G::ROWS + r;
+                    const float *po = p.part_o + ((int64_t)2 * cta0 * G::ROWS + r) * p.dim + 4 * d;
+                    const int64_t po_step = (int64_t)G::ROWS * p.dim;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                     float mr = -INFINITY, lr = 0.f;
-                    for (int i = lane; i < n; i += 32) mr = fmaxf(mr, __ldcg(p.part_ml + 2 * ((int64_t)slot_of(i) * rows_cta + r)));
-                    for (int off = 16; off; off >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xFFFFFFFFu, mr, off));
-                    for (int i = lane; i < n; i += 32) {
-                        const float *q = p.part_ml + 2 * ((int64_t)slot_of(i) * rows_cta + r);
-                        const float mc = __ldcg(q), f = mc == mr ? 1.f : exp2f(mc - mr);
-                        fac[i * nrow + r] = f;
-                        lr += f * __ldcg(q + 1);
+                    for (int c0 = 0; c0 < n; c0 += CH) {
+                        float2 q[CH];
+                        float4 u[CH];
+#pragma unroll
+                        for (int k = 0; k < CH; ++k) {
+                            const int sl = c0 + k == 0 ? 1 : 2 * (c0 + k);
+                            q[k] = make_float2(-INFINITY, 0.f);
+                            u[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (c0 + k < n) {
+                                q[k] = __ldcg(ml + sl * G::ROWS);
+                                u[k] = __ldcg(reinterpret_cast<const float4 *>(po + sl * po_step));
+                            }
+                        }
+                        float mn = mr;
+#pragma unroll
+                        for (int k = 0; k < CH; ++k) mn = fmaxf(mn, q[k].x);
+                        const float f0 = mr == mn ? 1.f : ex2(mr - mn);
+                        v.x *= f0; v.y *= f0; v.z *= f0; v.w *= f0;
+                        lr *= f0;
+                        mr = mn;
+#pragma unroll
+                        for (int k = 0; k < CH; ++k) {
+                            const float f = q[k].x == mn ? 1.f : ex2(q[k].x - mn);
+                            lr += f * q[k].y;
+                            v.x += f * u[k].x; v.y += f * u[k].y; v.z += f * u[k].z; v.w += f * u[k].w;
+                        }
                     }
-                    for (int off = 16; off; off >>= 1) lr += __shfl_xor_sync(0xFFFFFFFFu, lr, off);
-                    if (lane == 0) {
-                        s_lr[r] = lr;
-                        put_stats(r, mr, lr);
-                    }
-                }
-                __syncthreads();
-                for (int i = tid; i < nrow * p.dim; i += NT) {
-                    const int r = i / p.dim, d = i % p.dim;
-                    float v = 0.f;
-                    for (int c = 0; c < n; ++c) v += fac[c * nrow + r] * __ldcg(p.part_o + ((int64_t)slot_of(c) * rows_cta + r) * p.dim + d);
-                    put(r, d, s_lr[r] != 0.f ? v / s_lr[r] : 0.f);
+                    put(r, d, v, lr);
+                    if (d == 0) put_stats(r, mr, lr);
                 }
             }
         }
         __syncthreads();                                                  // the ring is refilled next
-        if (p.dim < DP && x < x1) {                                       // and its unused columns were written over
-            for (int i = tid; i < G::RING / 16; i += NT) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
-            __syncthreads();
-        }
     }
 }
 
 // score[s][h][j] (+)= sum over the rows of 2^(s_j - m) / l, from the raw scores
 // and the joined (m, l) that attn_decode_kernel left in the workspace.  One
 // thread per slot, rows in order.
-constexpr int ATT_SCORE_THREADS = 256;
+constexpr int ATT_SCORE_THREADS = 256, ATT_SCORE_ROWS = 256;
 
 static __global__ void __launch_bounds__(ATT_SCORE_THREADS) attn_score_kernel(const __grid_constant__ AttnParams p)
 {
+    __shared__ float2 s_st[ATT_SCORE_ROWS];                               // (m - l_shift, 1 / l; 0 for a row without weights)
     const int s = blockIdx.z, h = blockIdx.y;
     AttnSeq sq;
     sq.set(attn_len(p, s), p);
-    for (int64_t j64 = (int64_t)blockIdx.x * ATT_SCORE_THREADS + threadIdx.x; j64 < sq.len; j64 += (int64_t)gridDim.x * ATT_SCORE_THREADS) {
-        const int j = (int)j64;
-        if (!sq.seen(j)) continue;
-        const int64_t sh = (int64_t)s * p.n_kv + h;
-        const float *raw = p.raw + sh * p.rows * p.raw_stride + j;
-        const float *st = p.stats + 2 * sh * p.rows;
+    const int64_t sh = (int64_t)s * p.n_kv + h;
+    asm volatile("griddepcontrol.wait;" ::: "memory");                    // attn_decode_kernel is done
+    if ((int64_t)blockIdx.x * ATT_SCORE_THREADS >= sq.len) return;
+    for (int64_t b64 = (int64_t)blockIdx.x * ATT_SCORE_THREADS; b64 < sq.len; b64 += (int64_t)gridDim.x * ATT_SCORE_THREADS) {
+        const int j = (int)b64 + threadIdx.x;
+        const bool in = j < sq.len && sq.seen(j);
         float v = 0.f;
-        for (int r = 0; r < p.rows; ++r) {
-            const float m = __ldg(st + 2 * r), l = __ldg(st + 2 * r + 1);
-            if (l != 0.f) v += exp2f(__ldcg(raw + r * p.raw_stride) - m + p.l_shift) / l;
+        for (int r0 = 0; r0 < p.rows; r0 += ATT_SCORE_ROWS) {
+            const int nr = min(ATT_SCORE_ROWS, p.rows - r0);
+            __syncthreads();
+            for (int r = threadIdx.x; r < nr; r += ATT_SCORE_THREADS) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.stats) + sh * p.rows + r0 + r);
+                s_st[r] = make_float2(ml.x - p.l_shift, ml.y != 0.f ? __fdiv_rn(1.f, ml.y) : 0.f);
+            }
+            __syncthreads();
+            if (in) {
+                const float *raw = p.raw + (sh * p.raw_stride + j) * p.raw_rows + r0;
+                for (int r = 0; r < nr; r += 2) {
+                    const float2 u = __ldcg(reinterpret_cast<const float2 *>(raw + r));
+                    if (s_st[r].y != 0.f) v += ex2(u.x - s_st[r].x) * s_st[r].y;
+                    if (r + 1 < nr && s_st[r + 1].y != 0.f) v += ex2(u.y - s_st[r + 1].x) * s_st[r + 1].y;
+                }
+            }
         }
-        float *o = p.score + sh * p.score_stride + j;
-        *o = j >= sq.first ? v : *o + v;
+        if (in) {
+            float *o = p.score + sh * p.score_stride + j;
+            *o = j >= sq.first ? v : *o + v;
+        }
     }
 }
 
-// One launch of the instance that holds p.dim.
-template <int TYPE>
-static cudaError_t launch_attn(const AttnParams &p, int grid, cudaStream_t st)
+// One launch of the instance that holds p.dim and p.mb, on as many CTAs as run at
+// once and have a step by the longest lengths.
+template <int TYPE, int DP, int MB>
+static cudaError_t launch_attn_mb(const AttnParams &p, int sms, int64_t steps, cudaStream_t st)
 {
-    static SmemCfg configured[3];
-    if (p.dim <= 64) return launch_with(attn_decode_kernel<TYPE, 64>, configured[0], p, dim3((unsigned)grid), AttnGeom<TYPE, 64>::SMEM, st, false, false, AttnGeom<TYPE, 64>::THREADS);
-    if (p.dim <= 128) return launch_with(attn_decode_kernel<TYPE, 128>, configured[1], p, dim3((unsigned)grid), AttnGeom<TYPE, 128>::SMEM, st, false, false, AttnGeom<TYPE, 128>::THREADS);
-    return launch_with(attn_decode_kernel<TYPE, 256>, configured[2], p, dim3((unsigned)grid), AttnGeom<TYPE, 256>::SMEM, st, false, false, AttnGeom<TYPE, 256>::THREADS);
+    using G = AttnGeom<TYPE, DP, MB>;
+    static SmemCfg configured;
+    const int most = sms * G::CTAS < ATT_MAX_CTAS ? sms * G::CTAS : ATT_MAX_CTAS;
+    return launch_with(attn_decode_kernel<TYPE, DP, MB>, configured, p, dim3((unsigned)(steps < most ? steps : most)), G::SMEM, st, false, false, ATT_THREADS);
+}
+
+template <int TYPE>
+static cudaError_t launch_attn(const AttnParams &p, int sms, int64_t steps, cudaStream_t st)
+{
+    if (p.dim <= 64)
+        return p.mb == 1 ? launch_attn_mb<TYPE, 64, 1>(p, sms, steps, st) : p.mb == 2 ? launch_attn_mb<TYPE, 64, 2>(p, sms, steps, st) : launch_attn_mb<TYPE, 64, 4>(p, sms, steps, st);
+    if (p.dim <= 128)
+        return p.mb == 1 ? launch_attn_mb<TYPE, 128, 1>(p, sms, steps, st) : p.mb == 2 ? launch_attn_mb<TYPE, 128, 2>(p, sms, steps, st) : launch_attn_mb<TYPE, 128, 4>(p, sms, steps, st);
+    return p.mb == 1 ? launch_attn_mb<TYPE, 256, 1>(p, sms, steps, st) : launch_attn_mb<TYPE, 256, 2>(p, sms, steps, st);
 }
 
 }  // namespace qmv

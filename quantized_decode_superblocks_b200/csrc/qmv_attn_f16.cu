@@ -5,9 +5,9 @@
 
 namespace qmv {
 
-cudaError_t launch_attn_f16(const AttnParams &p, int grid, cudaStream_t st)
+cudaError_t launch_attn_f16(const AttnParams &p, int sms, int64_t steps, cudaStream_t st)
 {
-    return launch_attn<KV_F16>(p, grid, st);
+    return launch_attn<KV_F16>(p, sms, steps, st);
 }
 
 }  // namespace qmv

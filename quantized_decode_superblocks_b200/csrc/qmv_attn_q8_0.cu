@@ -5,9 +5,9 @@
 
 namespace qmv {
 
-cudaError_t launch_attn_q8_0(const AttnParams &p, int grid, cudaStream_t st)
+cudaError_t launch_attn_q8_0(const AttnParams &p, int sms, int64_t steps, cudaStream_t st)
 {
-    return launch_attn<KV_Q8_0>(p, grid, st);
+    return launch_attn<KV_Q8_0>(p, sms, steps, st);
 }
 
 }  // namespace qmv

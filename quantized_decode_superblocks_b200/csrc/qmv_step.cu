@@ -66,11 +66,12 @@ int page_shift(int page_size)
 }
 
 // Row blocks of 8: as many as one CTA takes.
-int attn_mt(int rows, int dim) { return rows <= 8 ? 1 : rows <= 16 ? 2 : attn_max_mt(dim); }
+int attn_mb(int rows, int dim) { return rows <= 8 ? 1 : rows <= 16 ? 2 : attn_max_mb(dim); }
 
 struct AttnWs {
     size_t ml, o, raw, stats, bytes;
-    int64_t raw_stride;
+    int64_t raw_stride, raw_rows;
+    int64_t steps;           // of the longest lengths, at most
 };
 
 // Workspace: counters | parts' (m, l) | parts' outputs | raw scores | rows' (m, l)
@@ -81,14 +82,17 @@ int attn_ws(int type, int head_dim, int n_kv, int n_head, int n_seq, int n_tok, 
     if (n_head < 1 || n_head > MAX_HEADS || n_head % n_kv) return QMV_ERR_SHAPE;
     const int rows = n_head / n_kv * n_tok;
     if (rows > MAX_GROUP_ROWS) return QMV_ERR_SHAPE;
-    if (n_seq * (slots / ATT_TILE + 2) > INT_MAX) return QMV_ERR_SHAPE;      // tiles of a head over all sequences
-    const size_t parts = (size_t)2 * ATT_MAX_CTAS * 8 * attn_mt(rows, head_dim);
+    const int mb = attn_mb(rows, head_dim);
+    w.steps = ceil_div(rows, 8 * mb) * n_seq * n_kv * (slots / (ATT_TILE * ATT_NW) + 2);
+    if (w.steps > INT_MAX) return QMV_ERR_SHAPE;
+    const size_t parts = (size_t)2 * ATT_MAX_CTAS * 8 * mb;
     w.raw_stride = ceil_div(slots, ATT_TILE) * ATT_TILE;
+    w.raw_rows = ceil_div(rows, 2) * 2;
     w.ml = up256(ATT_MAX_CTAS * sizeof(unsigned));
     w.o = w.ml + up256(parts * 2 * sizeof(float));
     w.raw = w.o + up256(parts * head_dim * sizeof(float));
     const size_t all_rows = (size_t)n_seq * n_kv * rows;
-    w.stats = w.raw + (score ? up256(all_rows * w.raw_stride * sizeof(float)) : 0);
+    w.stats = w.raw + (score ? up256((size_t)n_seq * n_kv * w.raw_rows * w.raw_stride * sizeof(float)) : 0);
     w.bytes = w.stats + (score ? up256(all_rows * 2 * sizeof(float)) : 0);
     return QMV_OK;
 }
@@ -158,13 +162,12 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     p.page_size = c.page_size;
     p.page_shift = page_shift(c.page_size);
     p.max_len = (int)(a->score ? std::min(slots, a->score_stride) : slots);
-    p.mt = attn_mt(p.rows, p.dim);
-    p.n_rb = (int)ceil_div(p.rows, 8 * p.mt);
+    p.mb = attn_mb(p.rows, p.dim);
+    p.n_rb = (int)ceil_div(p.rows, 8 * p.mb);
     p.window = a->window >= slots ? 0 : a->window;      // every slot is within a window that long
     p.n_sink = a->n_sink;
-    p.min_tiles = ATT_NW;
     p.scale_log2 = a->scale * 1.4426950408889634f;
-    p.l_shift = c.type == QMV_KV_F16 ? 15.f : 0.f;
+    p.l_shift = c.type == QMV_KV_F16 ? ATT_F16_SHIFT : 0.f;
     uint8_t *ws = static_cast<uint8_t *>(a->workspace);
     p.counters = reinterpret_cast<unsigned *>(ws);
     p.part_ml = reinterpret_cast<float *>(ws + w.ml);
@@ -172,17 +175,18 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     p.raw = reinterpret_cast<float *>(ws + w.raw);
     p.stats = reinterpret_cast<float *>(ws + w.stats);
     p.raw_stride = w.raw_stride;
+    p.raw_rows = (int)w.raw_rows;
     p.err = di.err;
 
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // one CTA per SM, and none that the longest lengths would leave without a tile
-    const int64_t tiles = (int64_t)p.n_seq * p.n_rb * p.n_kv * (slots / ATT_TILE + 2);
-    const int grid = (int)std::min<int64_t>(std::min(di.sm_count, ATT_MAX_CTAS), ceil_div(tiles, p.min_tiles));
-    cudaError_t e = c.type == QMV_KV_F16 ? launch_attn_f16(p, grid, st) : c.type == QMV_KV_BF16 ? launch_attn_bf16(p, grid, st) : launch_attn_q8_0(p, grid, st);
+    cudaError_t e = c.type == QMV_KV_F16    ? launch_attn_f16(p, di.sm_count, w.steps, st)
+                    : c.type == QMV_KV_BF16 ? launch_attn_bf16(p, di.sm_count, w.steps, st)
+                                            : launch_attn_q8_0(p, di.sm_count, w.steps, st);
     if (e != cudaSuccess || !p.score) return finish(e);
+    // launched while the first kernel runs (it waits for its end itself)
+    static SmemCfg configured;
     const unsigned gx = (unsigned)std::min<int64_t>(ceil_div(p.max_len, ATT_SCORE_THREADS), 1024);
-    attn_score_kernel<<<dim3(gx, (unsigned)p.n_kv, (unsigned)p.n_seq), ATT_SCORE_THREADS, 0, st>>>(p);
-    return finish(cudaGetLastError());
+    return finish(launch_with(attn_score_kernel, configured, p, dim3(gx, (unsigned)p.n_kv, (unsigned)p.n_seq), 0, st, true, false, ATT_SCORE_THREADS));
 }
 
 int kv_append(const qmv_append *a, qmv_stream_t stream)
