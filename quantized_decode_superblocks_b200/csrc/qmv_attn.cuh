@@ -29,7 +29,8 @@
 //   f16 cache:   q * 2^e (per row, so that the largest value is below 2^13) and
 //                2^9 * p as two f16 parts: 22 bits;
 //   bf16 cache:  q and p as three bf16 parts, 24 bits;
-//   Q8_0 cache:  q as for f16 (int8 is exact in f16), p * scale as for bf16.
+//   Q8_0 cache:  as for f16 (int8 is exact in it), with p * scale over a power
+//                of two for every 16 slots and 32 dims in the place of p.
 // Tensor cores cut off the bits that an accumulation shifts out, so a long chain of
 // them drifts: each tile's product starts from zero and is added to the
 // running output by rounded f32 adds.
@@ -59,7 +60,7 @@ constexpr int ATT_TILE = 16;                 // slots of a tile
 // parts: together below 2^16, and the second keeps what an f16 part cuts off
 // (half a step of its subnormals) below 2^-34 of the reference.  bf16 parts
 // have f32's range.
-__host__ __device__ constexpr float attn_slack(int type) { return type == 0 ? 6.f : 12.f; }
+__host__ __device__ constexpr float attn_slack(int type) { return type == 1 ? 12.f : 6.f; }
 constexpr float ATT_F16_SHIFT = 9.f;
 
 // 8-row blocks that one CTA takes at most: the outputs of 4 (2) of them fill half its registers
@@ -168,6 +169,19 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// c = a b, without an addend.
+template <bool BF16>
+__device__ __forceinline__ void mma_16_0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 template <bool BF16>
 __device__ __forceinline__ void mma_16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -208,11 +222,16 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint3
     mid = __byte_perm(vx, vy, 0x7632);
     lo = __byte_perm(__float_as_uint(rx - __uint_as_float(vx & 0xFFFF0000u)), __float_as_uint(ry - __uint_as_float(vy & 0xFFFF0000u)), 0x7632);
 }
-// (a, b) += (x, y) and (a, b) *= (x, y), one instruction each.
+// (a, b) += (x, y), *= (x, y), += (x, y) * f: one instruction each.
 __device__ __forceinline__ void add2(float &a, float &b, float x, float y)
 {
     asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
         : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void fma2(float &a, float &b, float x, float y, float f)
+{
+    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %4};\n\tfma.rn.f32x2 u, v, w, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y), "f"(f));
 }
 __device__ __forceinline__ void mul2(float &a, float &b, float x, float y)
 {
@@ -220,28 +239,18 @@ __device__ __forceinline__ void mul2(float &a, float &b, float x, float y)
         : "+f"(a), "+f"(b) : "f"(x), "f"(y));
 }
 
-// Four int8 of a word as two pairs of exact f16: the byte, its sign bit
-// flipped, under the exponent of 1024 is 1024 + 128 + value.
-__device__ __forceinline__ void i8_to_f16(uint32_t w, uint32_t &p01, uint32_t &p23)
+// Four int8 of a word as two pairs of exact f16 (bytes 0 and 1, 2 and 3 or as
+// the selectors say): the byte, its sign bit flipped, under the exponent of
+// 1024 is 1024 + 128 + value.
+template <int S0 = 0x4140, int S1 = 0x4342>
+__device__ __forceinline__ void i8_to_f16(uint32_t w, uint32_t &p0, uint32_t &p1)
 {
     w ^= 0x80808080u;
     const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
-    uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    uint32_t a = __byte_perm(w, 0x64646464u, S0), b = __byte_perm(w, 0x64646464u, S1);
     const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), off), y = __hsub2(*reinterpret_cast<__half2 *>(&b), off);
-    p01 = *reinterpret_cast<const uint32_t *>(&x);
-    p23 = *reinterpret_cast<const uint32_t *>(&y);
-}
-
-// Bytes (0, 2) and (1, 3) of a word as pairs of exact bf16: the low seven bits
-// under the exponent of 128, less 128 for a clear and 256 for a set sign bit.
-__device__ __forceinline__ void i8_to_bf16(uint32_t w, uint32_t &p02, uint32_t &p13)
-{
-    const uint32_t a = __byte_perm(w, 0x43434343u, 0x4240), b = __byte_perm(w, 0x43434343u, 0x4341);
-    const uint32_t am = a & 0xFF7FFF7Fu, as = a & 0xFF80FF80u, bm = b & 0xFF7FFF7Fu, bs = b & 0xFF80FF80u;
-    const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&am), *reinterpret_cast<const __nv_bfloat162 *>(&as));
-    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&bm), *reinterpret_cast<const __nv_bfloat162 *>(&bs));
-    p02 = *reinterpret_cast<const uint32_t *>(&x);
-    p13 = *reinterpret_cast<const uint32_t *>(&y);
+    p0 = *reinterpret_cast<const uint32_t *>(&x);
+    p1 = *reinterpret_cast<const uint32_t *>(&y);
 }
 
 // Shared-memory geometry of one instance: MB 8-row blocks of a DP-wide head.
@@ -259,7 +268,7 @@ struct AttnGeom {
     static constexpr int NST = STAGE >= 8 * 1024 ? 3 : STAGE >= 4 * 1024 ? 5 : 8;
     static constexpr int RING = ATT_NW * NST * STAGE;
     static constexpr int NPQ = TYPE == KV_BF16 ? 3 : 2;          // parts of q
-    static constexpr int NPP = TYPE == KV_F16 ? 2 : 3;           // parts of the weights
+    static constexpr int NPP = TYPE == KV_BF16 ? 3 : 2;          // parts of the weights
     static constexpr bool QREG = MB == 1 && DP <= 128;           // q's operand fragments in registers
     static constexpr int QW = 2 * NPQ;                           // words of q per lane and 16 columns
     static constexpr int Q_BYTES = QREG ? 0 : MB * (DP / 16) * 32 * QW * 4;
@@ -281,7 +290,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
 {
     using G = AttnGeom<TYPE, DP, MB>;
     constexpr int NW = ATT_NW, NT = ATT_THREADS, NPQ = G::NPQ, NPP = G::NPP, QW = G::QW;
-    constexpr bool PBF = TYPE != KV_F16;                         // type of the second product's parts
+    constexpr bool PBF = TYPE == KV_BF16;                        // type of the second product's parts
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_pref[ATT_MAX_SEQ + 1];                      // steps of one head before each sequence
     __shared__ int s_warp[NW];
@@ -352,7 +361,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
         sq.set(attn_len(p, s), p);
         const int seq0 = s_pref[s] * units;
         const int unit = (int)((unsigned)(x - seq0) / (unsigned)sq.n_steps);
-        const int rb = p.n_rb == 1 ? 0 : unit / p.n_kv, h = unit - rb * p.n_kv;
+        const int h = p.n_rb == 1 ? unit : unit / p.n_rb, rb = unit - h * p.n_rb;        // a head's row blocks follow each other: the cache is in L2
         const int seg0 = seq0 + unit * sq.n_steps, seg1 = seg0 + sq.n_steps;
         const int row0 = rb * G::ROWS;
         const int tile0 = (x - seg0) * NW + warp;                         // this warp's first tile
@@ -551,23 +560,23 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
                     const float d0 = half_bits_to_float(lds_u16(sa + g * G::SC_PITCH)), d1 = half_bits_to_float(lds_u16(sa + (g + 8) * G::SC_PITCH));
 #pragma unroll
                     for (int nb = 0; nb < MB; ++nb) {
-                        float hi[4] = {}, lo[4] = {};
-#pragma unroll
-                        for (int k2 = 0; k2 < 2; ++k2) {
-                            uint32_t q[QW];
-                            q_frag(nb, 2 * b + k2, q);
-                            mma_16<false>(hi, a[k2], q[0], q[1]);
-                            mma_16<false>(lo, a[k2], q[2], q[3]);
-                        }
-                        sc[nb][0] = fmaf(d0, hi[0] + lo[0], sc[nb][0]);
-                        sc[nb][1] = fmaf(d0, hi[1] + lo[1], sc[nb][1]);
-                        sc[nb][2] = fmaf(d1, hi[2] + lo[2], sc[nb][2]);
-                        sc[nb][3] = fmaf(d1, hi[3] + lo[3], sc[nb][3]);
+                        float hi[4], lo[4];
+                        uint32_t q[QW];
+                        q_frag(nb, 2 * b, q);
+                        mma_16_0<false>(hi, a[0], q[0], q[1]);
+                        mma_16_0<false>(lo, a[0], q[2], q[3]);
+                        q_frag(nb, 2 * b + 1, q);
+                        mma_16<false>(hi, a[1], q[0], q[1]);
+                        mma_16<false>(lo, a[1], q[2], q[3]);
+                        add2(hi[0], hi[1], lo[0], lo[1]);
+                        add2(hi[2], hi[3], lo[2], lo[3]);
+                        fma2(sc[nb][0], sc[nb][1], hi[0], hi[1], d0);
+                        fma2(sc[nb][2], sc[nb][3], hi[2], hi[3], d1);
                     }
                 }
             } else {
                 constexpr int PAR = MB == 1 ? 2 : 1;                      // chains per part: their sums wait on the one before
-                float a[MB][NPQ][PAR][4] = {};
+                float a[MB][NPQ][PAR][4];
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
                     uint32_t r[4];
@@ -577,7 +586,10 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
                         uint32_t q[QW];
                         q_frag(nb, ks, q);
 #pragma unroll
-                        for (int i = 0; i < NPQ; ++i) mma_16<TYPE == KV_BF16>(a[nb][i][ks % PAR], r, q[2 * i], q[2 * i + 1]);
+                        for (int i = 0; i < NPQ; ++i) {
+                            if (ks < PAR) mma_16_0<TYPE == KV_BF16>(a[nb][i][ks % PAR], r, q[2 * i], q[2 * i + 1]);
+                            else mma_16<TYPE == KV_BF16>(a[nb][i][ks % PAR], r, q[2 * i], q[2 * i + 1]);
+                        }
                     }
                 }
 #pragma unroll
@@ -683,27 +695,35 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
                         d[i] = half_bits_to_float(lds_u16(sa + (2 * c4 + (i & 1) + (i >> 1) * 8) * G::SC_PITCH));
                         if (mixed && !(fabsf(d[i]) < INFINITY)) d[i] = 0.f;       // NaN of a slot that this row may not see: its weight is 0
                     }
+                    // the scales over a power of two at least the largest of them: their products with the weights stay in f16
+                    float dm = fmaxf(fmaxf(fabsf(d[0]), fabsf(d[1])), fmaxf(fabsf(d[2]), fabsf(d[3])));
+                    dm = fmaxf(dm, __shfl_xor_sync(0xFFFFFFFFu, dm, 1));
+                    dm = fmaxf(dm, __shfl_xor_sync(0xFFFFFFFFu, dm, 2));
+                    const uint32_t ex = min(__float_as_uint(dm) >> 23, 200u);
+                    const float down = __uint_as_float((253u - ex) << 23), back = __uint_as_float((ex + 1u) << 23);
+                    mul2(d[0], d[1], down, down);
+                    mul2(d[2], d[3], down, down);
                     uint32_t a[2][4];
 #pragma unroll
                     for (int k2 = 0; k2 < 2; ++k2) {                      // rows g and g + 8: dims 2 g and 2 g + 1 of 16
-                        i8_to_bf16(r[2 * k2], a[k2][0], a[k2][1]);
-                        i8_to_bf16(r[2 * k2 + 1], a[k2][2], a[k2][3]);
+                        i8_to_f16<0x4240, 0x4341>(r[2 * k2], a[k2][0], a[k2][1]);
+                        i8_to_f16<0x4240, 0x4341>(r[2 * k2 + 1], a[k2][2], a[k2][3]);
                     }
 #pragma unroll
                     for (int nb = 0; nb < MB; ++nb) {
-                        float pd[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) pd[i] = pw[nb][i] * d[i];
-                        uint32_t pb[3][2];
-                        split_bf16(pd[0], pd[1], pb[0][0], pb[1][0], pb[2][0]);
-                        split_bf16(pd[2], pd[3], pb[0][1], pb[1][1], pb[2][1]);
+                        float pd[4] = {pw[nb][0], pw[nb][1], pw[nb][2], pw[nb][3]};
+                        mul2(pd[0], pd[1], d[0], d[1]);
+                        mul2(pd[2], pd[3], d[2], d[3]);
+                        uint32_t pb[2][2];
+                        split_f16(pd[0], pd[1], pb[0][0], pb[1][0]);
+                        split_f16(pd[2], pd[3], pb[0][1], pb[1][1]);
 #pragma unroll
                         for (int k2 = 0; k2 < 2; ++k2) {
-                            float t[4] = {};
-#pragma unroll
-                            for (int i = 2; i >= 0; --i) mma_16<true>(t, a[k2], pb[i][0], pb[i][1]);
-                            add2(acc[nb][2 * b + k2][0], acc[nb][2 * b + k2][1], t[0], t[1]);
-                            add2(acc[nb][2 * b + k2][2], acc[nb][2 * b + k2][3], t[2], t[3]);
+                            float t[4];
+                            mma_16_0<false>(t, a[k2], pb[1][0], pb[1][1]);
+                            mma_16<false>(t, a[k2], pb[0][0], pb[0][1]);
+                            fma2(acc[nb][2 * b + k2][0], acc[nb][2 * b + k2][1], t[0], t[1], back);
+                            fma2(acc[nb][2 * b + k2][2], acc[nb][2 * b + k2][3], t[2], t[3], back);
                         }
                     }
                 }
@@ -726,9 +746,10 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
                         ldsm4t(r, va + G::at(v_row, 2 * i + v_chunk));
 #pragma unroll
                         for (int nb = 0; nb < MB; ++nb) {
-                            float t[4] = {};
+                            float t[4];
+                            mma_16_0<PBF>(t, r, pb[nb][NPP - 1][0], pb[nb][NPP - 1][1]);
 #pragma unroll
-                            for (int k = NPP - 1; k >= 0; --k) mma_16<PBF>(t, r, pb[nb][k][0], pb[nb][k][1]);
+                            for (int k = NPP - 2; k >= 0; --k) mma_16<PBF>(t, r, pb[nb][k][0], pb[nb][k][1]);
                             add2(acc[nb][i][0], acc[nb][i][1], t[0], t[1]);
                             add2(acc[nb][i][2], acc[nb][i][3], t[2], t[3]);
                         }
@@ -751,9 +772,10 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
                             r[0] &= z[0]; r[1] &= z[0]; r[2] &= z[1]; r[3] &= z[1];
 #pragma unroll
                             for (int nb = 0; nb < MB; ++nb) {
-                                float t[4] = {};
+                                float t[4];
+                                mma_16_0<PBF>(t, r, pb[nb][NPP - 1][0], pb[nb][NPP - 1][1]);
 #pragma unroll
-                                for (int k = NPP - 1; k >= 0; --k) mma_16<PBF>(t, r, pb[nb][k][0], pb[nb][k][1]);
+                                for (int k = NPP - 2; k >= 0; --k) mma_16<PBF>(t, r, pb[nb][k][0], pb[nb][k][1]);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
                                     if (s_at[nb * 8 + 2 * c4 + (e & 1)] == at) acc[nb][i][e] += t[e];

@@ -231,6 +231,18 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
+// One 1-D bulk copy this CTA's shared memory -> global (16-byte aligned, a
+// multiple of 16 bytes), and the wait until this thread's copies have read
+// their sources.
+__device__ __forceinline__ void bulk_s2g(void *dst, uint32_t src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" :: "l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_s2g_drain()
+{
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 // An L2 policy that evicts the lines it tags first: for weights, which a
 // decode step reads once, so that streaming them does not push the
 // activations and the kernels' code out of L2.

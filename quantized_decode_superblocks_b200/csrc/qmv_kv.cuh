@@ -2,7 +2,6 @@
 // cache for each sequence (kv_evict); both declared in include/qmv.h.
 #pragma once
 
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "qmv_attn.cuh"
@@ -102,16 +101,24 @@ static __global__ void __launch_bounds__(APP_THREADS) kv_append_kernel(const __g
 }
 
 // -------------------------------------------------------------- evict --
-// A cluster of EV_CL CTAs per (sequence, kv head); CTA r looks after the r-th
-// part of the slots.  The slots between the kept ends are ranked by a radix
-// select over order-preserving 32-bit keys (four 8-bit digits, highest first):
-// each CTA counts its own slots' digits, and all add up the cluster's counts
-// over distributed shared memory, so that the key of the last slot to keep, and how
-// many slots with exactly that key are kept (the lowest ones), are known to
-// all after four rounds.  Then each CTA writes its kept slots in order, at
-// the place that the counts of the CTAs before it give, and the cluster copies
-// the kept slots' values, an equal share per CTA.
-constexpr int EV_CL = 8, EV_THREADS = 512;
+// Two kernels: the choice, bound by latency, and the copy, bound by bandwidth;
+// apart, so that the copy has every SM to itself and is spread evenly.
+//
+// Choice: a CTA per (sequence, kv head).  The slots between the kept ends are
+// ranked by a radix select over order-preserving 32-bit keys (digits of 11, 11
+// and 10 bits, highest first), which gives the key of the last slot to keep and
+// how many slots with exactly that key are kept (the lowest ones).  A round that
+// leaves no slot undecided is the last one: scores that all differ need two.
+// Then each warp writes the kept slots of its part in order, at the place that
+// the counts of the warps before it give.  (Spread over a cluster of 8 CTAs,
+// the counts' way through distributed shared memory cost more than it saved:
+// 4352 slots 7.6 us, 16 x 8 x 16384 slots 10 us, against FIXME here.)
+//
+// Copy: a warp per 32 (rows over 256 bytes: 16) kept slots of a (sequence, head),
+// the heads of the same slots next to each other.
+constexpr int EV_THREADS = 1024, EV_BINS = 2048;
+constexpr int EV_KEYS = 40960;                // keys that shared memory holds; those of later slots are made anew in every round
+constexpr int EV_COPY_THREADS = 128;
 
 struct EvictParams {
     uint8_t *k, *v, *ks, *vs;
@@ -123,6 +130,7 @@ struct EvictParams {
     int32_t *kept, *len_out;
     int32_t n_kv, page_size, max_len, keep_first, keep_last, budget;
     int32_t row_bytes, scale_words, eb;       // of one slot and head; scale_words: 4-byte words of its scales
+    int32_t copy_slots;                       // of a warp of the copy
     int *err;
 };
 
@@ -134,16 +142,14 @@ __device__ __forceinline__ uint32_t evict_key(float x)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-static __global__ void __cluster_dims__(EV_CL, 1, 1) __launch_bounds__(EV_THREADS) kv_evict_kernel(const __grid_constant__ EvictParams p)
+static __global__ void __launch_bounds__(EV_THREADS) kv_evict_kernel(const __grid_constant__ EvictParams p)
 {
-    namespace cg = cooperative_groups;
-    cg::cluster_group cl = cg::this_cluster();
-    __shared__ int s_hist[4][256];
-    __shared__ int s_cnt[2];                  // this CTA's slots above, and at, the last key
-    __shared__ int s_sum[256];
-    __shared__ int s_sel[2];
-    __shared__ int s_warp[EV_THREADS / 32][2];
-    const int rank = (int)cl.block_rank(), h = blockIdx.y, s = blockIdx.z;
+    constexpr int NW = EV_THREADS / 32, PER = EV_BINS / EV_THREADS, FLY = 8;      // FLY: loads of a thread in flight
+    static_assert(NW == 32 && PER == 2, "one warp reads the warps' counts; a thread has two digits");
+    __shared__ __align__(16) int s_hist[EV_BINS];
+    __shared__ int s_sel[3];
+    __shared__ int s_up[NW], s_eq[NW];
+    const int h = blockIdx.x, s = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int raw = __ldg(p.kv_len + s), n = min(max(raw, 0), p.max_len), m = min(n, p.budget);
     if (raw != n && tid == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
@@ -151,154 +157,181 @@ static __global__ void __cluster_dims__(EV_CL, 1, 1) __launch_bounds__(EV_THREAD
     const float *score = p.score + sh * p.score_stride;
     float *score_out = p.score_out + sh * p.score_out_stride;
     int32_t *kept = p.kept + sh * p.budget;
-    const int part = (int)(((int64_t)n + EV_CL * EV_THREADS - 1) / (EV_CL * EV_THREADS)) * EV_THREADS;
-    const int a = (int)min((int64_t)n, (int64_t)rank * part), b = (int)min((int64_t)n, (int64_t)a + part);
     const int mid0 = min(p.keep_first, n), mid1 = max(mid0, n - p.keep_last);     // ranked slots
     const bool all = n <= p.budget;
-    const int need = p.budget - p.keep_first - p.keep_last;                       // of them (not all)
 
-    uint32_t prefix = 0;
-    int want = need;                                                              // still to take within the prefix
+    extern __shared__ __align__(16) uint32_t s_key[];                             // [min(slots, EV_KEYS)], the largest for the kept ends
+    auto key_at = [&](int j, float x) { return j < mid0 || j >= mid1 ? 0xFFFFFFFFu : evict_key(x); };
+    auto key_of = [&](int j) { return j < EV_KEYS ? s_key[j] : key_at(j, __ldg(score + j)); };
+    uint32_t prefix = 0xFFFFFFFFu;            // no ranked key is that large
+    int shift = 0, want = p.budget - p.keep_first - p.keep_last;                  // still to take within the prefix
+    bool ties = false;                                                            // only some of the slots with the last key are kept
     if (!all) {
-        for (int i = tid; i < 4 * 256; i += EV_THREADS) (&s_hist[0][0])[i] = 0;
+        reinterpret_cast<int2 *>(s_hist)[tid] = make_int2(0, 0);
         __syncthreads();
-        const int c0 = max(a, mid0), c1 = min(b, mid1);
-        for (int pass = 0; pass < 4; ++pass) {
-            const int sft = 24 - 8 * pass;
-            for (int j = c0 + tid; j < c1; j += EV_THREADS) {
-                const uint32_t key = evict_key(__ldg(score + j));
-                if (pass == 0 || (key >> (sft + 8)) == prefix) atomicAdd(&s_hist[pass][(key >> sft) & 255u], 1);
-            }
-            cl.sync();
-            if (tid < 256) {
-                int c = 0;
-                for (int r = 0; r < EV_CL; ++r) c += cl.map_shared_rank(&s_hist[0][0], r)[pass * 256 + tid];
-                s_sum[tid] = c;
-            }
-            __syncthreads();
-            if (warp == 0) {
-                // lane i has digits 255 - 8 i and the seven below: from the top down
-                int own = 0;
-                for (int d = 0; d < 8; ++d) own += s_sum[255 - 8 * lane - d];
-                int up = own;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xFFFFFFFFu, up, o);
-                    if (lane >= o) up += y;
-                }
-                int before = up - own;                                            // slots of larger digits
-                if (before < want && up >= want) {
-                    for (int d = 0; d < 8; ++d) {
-                        const int dig = 255 - 8 * lane - d, c = s_sum[dig];
-                        if (before + c >= want) {
-                            s_sel[0] = dig;
-                            s_sel[1] = want - before;
-                            break;
-                        }
-                        before += c;
-                    }
-                }
-                if (want == 0 && lane == 0) {                                     // nothing between the ends is kept
-                    s_sel[0] = 255;
-                    s_sel[1] = 0;
+        for (int64_t j0 = tid; j0 < n; j0 += FLY * EV_THREADS) {                  // keys, and the counts of their first digit
+            float x[FLY];
+#pragma unroll
+            for (int u = 0; u < FLY; ++u) x[u] = j0 + u * EV_THREADS < n ? __ldg(score + j0 + u * EV_THREADS) : 0.f;
+#pragma unroll
+            for (int u = 0; u < FLY; ++u) {
+                const int64_t j = j0 + u * EV_THREADS;
+                if (j < n) {
+                    const uint32_t key = key_at((int)j, x[u]);
+                    if (j < EV_KEYS) s_key[j] = key;
+                    if (key != 0xFFFFFFFFu) atomicAdd(s_hist + (key >> 21), 1);
                 }
             }
-            __syncthreads();
-            prefix = (prefix << 8) | (uint32_t)s_sel[0];
-            want = s_sel[1];
-            __syncthreads();
         }
-    }
-    // ---- how many slots this CTA keeps, and its place among the cluster's
-    auto is_end = [&](int j) { return all || j < mid0 || j >= mid1; };
-    int above = 0, at = 0;
-    for (int j = a + tid; j < b; j += EV_THREADS) {
-        const uint32_t key = all ? 0u : evict_key(__ldg(score + j));
-        above += is_end(j) || (need > 0 && key > prefix);
-        at += !is_end(j) && key == prefix;
-    }
-    for (int o = 16; o; o >>= 1) {
-        above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
-        at += __shfl_xor_sync(0xFFFFFFFFu, at, o);
-    }
-    if (lane == 0) {
-        s_warp[warp][0] = above;
-        s_warp[warp][1] = at;
+        for (int pass = 0; pass < 3 && want > 0; ++pass) {
+            const int above = shift;                                              // the digits that are decided lie above this bit
+            shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            if (pass) {
+                const uint32_t digits = pass == 1 ? 2047u : 1023u;
+                reinterpret_cast<int2 *>(s_hist)[tid] = make_int2(0, 0);
+                __syncthreads();
+#pragma unroll 4
+                for (int64_t j = mid0 + tid; j < mid1; j += EV_THREADS) {
+                    const uint32_t key = key_of((int)j);
+                    if ((key >> above) == prefix) atomicAdd(s_hist + ((key >> shift) & digits), 1);
+                }
+            }
+            __syncthreads();
+            // this thread's two digits, from the top down
+            const int lo = EV_BINS - PER * (tid + 1);
+            const int2 c = *reinterpret_cast<const int2 *>(s_hist + lo);
+            int up = c.x + c.y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, up, o);
+                if (lane >= o) up += y;
+            }
+            if (lane == 31) s_up[warp] = up;
+            __syncthreads();
+            int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s_up[lane] : 0);       // slots of larger digits: the warps' before,
+            before += up - c.x - c.y;                                             // and this one's
+            if (before < want && before + c.x + c.y >= want) {
+                const bool first = before + c.y >= want;
+                s_sel[0] = lo + (first ? 1 : 0);
+                s_sel[1] = want - before - (first ? 0 : c.y);
+                s_sel[2] = first ? c.y : c.x;
+            }
+            __syncthreads();
+            prefix = pass == 0 ? (uint32_t)s_sel[0] : (prefix << (above - shift)) | (uint32_t)s_sel[0];
+            want = s_sel[1];
+            ties = s_sel[2] != want;
+            if (!ties) break;                                                     // all of that digit are kept
+        }
     }
     __syncthreads();
-    if (tid < 2) {
-        int c = 0;
-        for (int w = 0; w < EV_THREADS / 32; ++w) c += s_warp[w][tid];
-        s_cnt[tid] = c;
+    // ---- how many slots each warp keeps, and its place.  Without ties what is
+    // kept are the keys from the last one up.
+    const uint32_t least = all ? 0u : prefix << shift;
+    const int chunk = (int)(((int64_t)n + EV_THREADS - 1) / EV_THREADS) * 32;     // slots of a warp
+    const int w0 = (int)min((int64_t)n, (int64_t)warp * chunk), w1 = (int)min((int64_t)n, (int64_t)w0 + chunk);
+    int n_up = 0, n_eq = 0;
+    if (all) {
+        n_up = lane == 0 ? w1 - w0 : 0;
+    } else if (!ties) {
+#pragma unroll 4
+        for (int j = w0 + lane; j < w1; j += 32) n_up += key_of(j) >= least;
+    } else {
+        for (int j = w0 + lane; j < w1; j += 32) {
+            const uint32_t key = key_of(j);
+            n_up += key > least;                                                  // ties are decided by all 32 bits
+            n_eq += key == least;
+        }
     }
-    cl.sync();
-    int pre_above = 0, pre_at = 0;
-    for (int r = 0; r < rank; ++r) {
-        const int *c = cl.map_shared_rank(s_cnt, r);
-        pre_above += c[0];
-        pre_at += c[1];
+    n_up = __reduce_add_sync(0xFFFFFFFFu, n_up);
+    n_eq = __reduce_add_sync(0xFFFFFFFFu, n_eq);
+    if (lane == 0) {
+        s_up[warp] = n_up;
+        s_eq[warp] = n_eq;
     }
+    __syncthreads();
+    int bu = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s_up[lane] : 0);        // kept, and at the last key, before this warp
+    int be = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s_eq[lane] : 0);
     // ---- the kept slots in order
-    for (int j0 = a; j0 < b; j0 += EV_THREADS) {
-        const int j = j0 + tid;
-        float sc = 0.f;
-        bool up = false, eq = false;
-        if (j < b) {
-            sc = __ldg(score + j);
-            const uint32_t key = evict_key(sc);
-            up = is_end(j) || (need > 0 && key > prefix);
-            eq = !is_end(j) && key == prefix;
-        }
-        const uint32_t mu = __ballot_sync(0xFFFFFFFFu, up), me = __ballot_sync(0xFFFFFFFFu, eq);
-        __syncthreads();
-        if (lane == 0) {
-            s_warp[warp][0] = __popc(mu);
-            s_warp[warp][1] = __popc(me);
-        }
-        __syncthreads();
-        int bu = pre_above, be = pre_at;
-        for (int w = 0; w < EV_THREADS / 32; ++w) {
-            if (w < warp) {
-                bu += s_warp[w][0];
-                be += s_warp[w][1];
+    const uint32_t below = (1u << lane) - 1u;
+    if (!ties) {
+#pragma unroll 4
+        for (int j = w0 + lane; j - lane < w1; j += 32) {
+            const bool up = j < w1 && (all || key_of(j) >= least);
+            const uint32_t mu = __ballot_sync(0xFFFFFFFFu, up);
+            if (up) {
+                const int i = bu + __popc(mu & below);
+                kept[i] = j;
+                score_out[i] = __ldg(score + j);
             }
-            pre_above += s_warp[w][0];
-            pre_at += s_warp[w][1];
+            bu += __popc(mu);
         }
-        const uint32_t below = (1u << lane) - 1u;
-        bu += __popc(mu & below);
-        be += __popc(me & below);
-        if (up || (eq && be < want)) {
-            const int i = bu + min(be, want);
-            kept[i] = j;
-            score_out[i] = sc;
+    } else {
+        for (int j = w0 + lane; j - lane < w1; j += 32) {
+            const uint32_t key = j < w1 ? key_of(j) : 0u;
+            const bool up = j < w1 && key > least, eq = j < w1 && key == least;
+            const uint32_t mu = __ballot_sync(0xFFFFFFFFu, up), me = __ballot_sync(0xFFFFFFFFu, eq);
+            const int e = be + __popc(me & below);
+            if (up || (eq && e < want)) {
+                const int i = bu + __popc(mu & below) + min(e, want);
+                kept[i] = j;
+                score_out[i] = __ldg(score + j);
+            }
+            bu += __popc(mu);
+            be += __popc(me);
         }
     }
-    if (rank == 0 && h == 0 && tid == 0) p.len_out[s] = m;
-    cl.sync();                                                                    // the list is complete
-    // ---- copy: 16-byte pieces of k and v, 4-byte words of the scales
-    const int32_t *src = p.table + (int64_t)s * p.table_stride, *dst = p.dst_table + (int64_t)s * p.dst_table_stride;
-    const int i0 = (int)((int64_t)m * rank / EV_CL), i1 = (int)((int64_t)m * (rank + 1) / EV_CL);
-    const int pieces = p.row_bytes / 16;
-    for (int i = i0 + warp; i < i1; i += EV_THREADS / 32) {
-        const int j = __ldcg(kept + i);
-        const int ps = __ldg(src + j / p.page_size), pd = __ldg(dst + i / p.page_size);
-        const bool ok = ps >= 0 && ps < p.n_pages && pd >= 0 && pd < p.n_pages;
-        if (!ok) {
-            if (lane == 0) atomicOr(p.err, 8 /* QMV_DEVERR_PAGE_ID */);
-            continue;
+    if (h == 0 && tid == 0) p.len_out[s] = m;
+}
+
+// A lane per slot: its rows of k and v go through shared memory by bulk copies,
+// its scales (too short for one) through registers.
+static __global__ void __launch_bounds__(EV_COPY_THREADS) kv_evict_copy_kernel(const __grid_constant__ EvictParams p)
+{
+    extern __shared__ __align__(128) uint8_t s_rows[];                            // [warps][slots][k | v]
+    __shared__ __align__(8) uint64_t s_bar[EV_COPY_THREADS / 32];
+    const int h = blockIdx.x % p.n_kv, s = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int m = min(min(max(__ldg(p.kv_len + s), 0), p.max_len), p.budget);
+    const int i = (blockIdx.x / p.n_kv * (EV_COPY_THREADS / 32) + warp) * p.copy_slots + lane;
+    const bool in = lane < p.copy_slots && i < m;
+    const int pd = in ? __ldg(p.dst_table + (int64_t)s * p.dst_table_stride + i / p.page_size) : -1;
+    const uint32_t bar = smem_addr(s_bar + warp);
+    if (lane == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");                            // kv_evict_kernel is done
+    int64_t es = 0, ed = 0;
+    bool ok = false;
+    if (in) {
+        const int j = __ldcg(p.kept + ((int64_t)s * p.n_kv + h) * p.budget + i);
+        const int ps = __ldg(p.table + (int64_t)s * p.table_stride + j / p.page_size);
+        ok = ps >= 0 && ps < p.n_pages && pd >= 0 && pd < p.n_pages;
+        if (!ok) atomicOr(p.err, 8 /* QMV_DEVERR_PAGE_ID */);
+        es = ps * p.page_stride + h * p.head_stride + (j % p.page_size) * p.slot_stride;
+        ed = pd * p.page_stride + h * p.head_stride + (i % p.page_size) * p.slot_stride;
+    }
+    const uint32_t n_ok = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, ok)), rb = (uint32_t)p.row_bytes;
+    if (n_ok == 0) return;
+    const uint32_t row = smem_addr(s_rows) + (uint32_t)(warp * p.copy_slots + lane) * 2 * rb;
+    if (lane == 0) mbar_arrive_expect_tx(bar, n_ok * 2 * rb);
+    __syncwarp();
+    if (ok) {
+        bulk_g2s(row, p.k + es * p.eb, rb, bar);
+        bulk_g2s(row + rb, p.v + es * p.eb, rb, bar);
+        for (int c = 0; c < p.scale_words; ++c) {
+            const uint32_t x = __ldg(reinterpret_cast<const uint32_t *>(p.ks + es / 16) + c);
+            const uint32_t y = __ldg(reinterpret_cast<const uint32_t *>(p.vs + es / 16) + c);
+            reinterpret_cast<uint32_t *>(p.ks + ed / 16)[c] = x;
+            reinterpret_cast<uint32_t *>(p.vs + ed / 16)[c] = y;
         }
-        const int64_t es = ps * p.page_stride + h * p.head_stride + (j % p.page_size) * p.slot_stride;
-        const int64_t ed = pd * p.page_stride + h * p.head_stride + (i % p.page_size) * p.slot_stride;
-        for (int c = lane; c < 2 * pieces; c += 32) {
-            uint8_t *pool = c < pieces ? p.k : p.v;
-            const int64_t o = (c < pieces ? c : c - pieces) * 16;
-            *reinterpret_cast<uint4 *>(pool + ed * p.eb + o) = __ldcg(reinterpret_cast<const uint4 *>(pool + es * p.eb + o));
-        }
-        for (int c = lane; c < 2 * p.scale_words; c += 32) {
-            uint8_t *pool = c < p.scale_words ? p.ks : p.vs;
-            const int64_t o = (c < p.scale_words ? c : c - p.scale_words) * 4;
-            *reinterpret_cast<uint32_t *>(pool + ed / 16 + o) = __ldcg(reinterpret_cast<const uint32_t *>(pool + es / 16 + o));
-        }
+    }
+    if (!mbar_wait_bounded(bar, 0)) {
+        atomicOr(p.err, mbar_wait_bounded(bar, 0) ? 2 : 2 | 4 /* QMV_DEVERR_TIMEOUT, QMV_DEVERR_DRAIN */);
+        return;
+    }
+    if (ok) {
+        bulk_s2g(p.k + ed * p.eb, row, rb);
+        bulk_s2g(p.v + ed * p.eb, row + rb, rb);
+        bulk_s2g_drain();
     }
 }
 

@@ -167,7 +167,7 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     p.window = a->window >= slots ? 0 : a->window;      // every slot is within a window that long
     p.n_sink = a->n_sink;
     p.scale_log2 = a->scale * 1.4426950408889634f;
-    p.l_shift = c.type == QMV_KV_F16 ? ATT_F16_SHIFT : 0.f;
+    p.l_shift = c.type == QMV_KV_BF16 ? 0.f : ATT_F16_SHIFT;
     uint8_t *ws = static_cast<uint8_t *>(a->workspace);
     p.counters = reinterpret_cast<unsigned *>(ws);
     p.part_ml = reinterpret_cast<float *>(ws + w.ml);
@@ -300,9 +300,18 @@ int kv_evict(const qmv_evict *a, qmv_stream_t stream)
     p.eb = c.type == QMV_KV_Q8_0 ? 1 : 2;
     p.row_bytes = c.head_dim * p.eb;
     p.scale_words = c.type == QMV_KV_Q8_0 ? c.head_dim / 64 : 0;
+    p.copy_slots = p.row_bytes <= 256 ? 32 : 16;
     p.err = di.err;
-    kv_evict_kernel<<<dim3(EV_CL, (unsigned)c.n_kv_head, (unsigned)a->n_seq), EV_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return finish(cudaGetLastError());
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    static SmemCfg configured_choice, configured;
+    const size_t smem = (size_t)std::min(p.max_len, EV_KEYS) * sizeof(uint32_t);
+    const cudaError_t e = launch_with(kv_evict_kernel, configured_choice, p, dim3((unsigned)c.n_kv_head, (unsigned)a->n_seq), smem, st, false, false, EV_THREADS);
+    if (e != cudaSuccess) return finish(e);
+    // launched while the choice runs (it waits for its end itself)
+    const int per = EV_COPY_THREADS / 32 * p.copy_slots;
+    const int64_t gx = ceil_div(std::min(p.budget, p.max_len), per) * c.n_kv_head;           // at most 2^31 / 64 * 1024 / 16: budget slots fit the table
+    if (gx > INT_MAX) return QMV_ERR_SHAPE;
+    return finish(launch_with(kv_evict_copy_kernel, configured, p, dim3((unsigned)gx, (unsigned)a->n_seq), (size_t)per * 2 * p.row_bytes, st, true, false, EV_COPY_THREADS));
 }
 
 size_t logits_ws_bytes(int n_rows)
@@ -350,9 +359,11 @@ int logits_argmax(const qmv_logits *a, qmv_stream_t stream)
     p.idx = a->idx_out;
     p.keys = static_cast<unsigned long long *>(a->workspace);
     p.done = reinterpret_cast<unsigned *>(p.keys + a->n_rows);
-    const dim3 grid((unsigned)ceil_div(a->vocab, LG_SLICE), (unsigned)a->n_rows);
-    logits_argmax_kernel<<<grid, LG_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return finish(cudaGetLastError());
+    p.slice = logits_slice(a->n_rows, a->vocab, di.sm_count);
+    const dim3 grid((unsigned)ceil_div(a->vocab, p.slice), (unsigned)a->n_rows);
+    static SmemCfg configured;
+    const size_t smem = p.hist || p.bias_ids ? (size_t)p.slice * sizeof(int2) : 0;
+    return finish(launch_with(logits_argmax_kernel, configured, p, grid, smem, reinterpret_cast<cudaStream_t>(stream), false, false, LG_THREADS));
 }
 
 }  // extern "C"

@@ -108,8 +108,10 @@ class KvCache(ctypes.Structure):
 
 
 class _Args(ctypes.Structure):
+    _name = None
+
     def _begin(self, cache=None):
-        self._held, self._device = [], None
+        self._held, self._device, self._entry = [], None, None
         if cache is not None:
             self._held.append(cache)
             self._device = cache._device
@@ -124,6 +126,7 @@ class _Args(ctypes.Structure):
 class AppendArgs(_Args):
     """kv_append: q [n_seq, n_tok, n_head * head_dim] or None, k and v [.., n_kv_head * head_dim] (f32; slices
     of one fused product are fine) into the cache; q_out as q, or q itself to rotate in place."""
+    _name = "kv_append"
     _fields_ = [("cache", KvCache), ("q", _vp), ("k_in", _vp), ("v_in", _vp), ("q_out", _vp), ("q_stride", _i64),
                 ("k_stride", _i64), ("v_stride", _i64), ("q_out_stride", _i64), ("n_head", _i32), ("n_seq", _i32),
                 ("n_tok", _i32), ("rope_dim", _i32), ("rope_style", _i32), ("max_pages", _i32), ("table_stride", _i64),
@@ -160,6 +163,7 @@ class AppendArgs(_Args):
 class AttnArgs(_Args):
     """attn_decode: q and out [n_seq, n_tok, n_head * head_dim] f32, score [n_seq, n_kv_head, slots] f32 or None,
     workspace: a zeroed uint8 tensor of at least attn_ws_bytes()."""
+    _name = "attn_decode"
     _fields_ = [("cache", KvCache), ("q", _vp), ("out", _vp), ("score", _vp), ("q_stride", _i64), ("out_stride", _i64),
                 ("score_stride", _i64), ("n_head", _i32), ("n_seq", _i32), ("n_tok", _i32), ("max_pages", _i32),
                 ("table_stride", _i64), ("block_table", _vp), ("kv_len", _vp), ("scale", _f32), ("window", _i32),
@@ -189,6 +193,7 @@ class AttnArgs(_Args):
 class EvictArgs(_Args):
     """kv_evict: score [n_seq, n_kv_head, slots], kept int32 and score_out f32 [n_seq, n_kv_head, budget],
     len_out int32 [n_seq]; the kept slots go to the pages of dst_table."""
+    _name = "kv_evict"
     _fields_ = [("cache", KvCache), ("score", _vp), ("score_out", _vp), ("score_stride", _i64),
                 ("score_out_stride", _i64), ("n_seq", _i32), ("max_pages", _i32), ("dst_max_pages", _i32),
                 ("keep_first", _i32), ("keep_last", _i32), ("budget", _i32), ("table_stride", _i64),
@@ -220,6 +225,7 @@ class LogitsArgs(_Args):
     [n_rows, n] with hist_len [n_rows] and params [n_rows, 3] (or all None), bias_ids / bias_vals [n_rows, n]
     with bias_len, mask int32 [n_rows, >= ceil(vocab / 32)] of bits, idx_out int32 [n_rows], workspace: a
     zeroed uint8 tensor of at least logits_ws_bytes(n_rows)."""
+    _name = "logits_argmax"
     _fields_ = [("logits", _vp), ("out", _vp), ("logits_stride", _i64), ("out_stride", _i64), ("n_rows", _i32),
                 ("vocab", _i32), ("hist", _vp), ("hist_len", _vp), ("hist_stride", _i64), ("params", _vp),
                 ("bias_ids", _vp), ("bias_len", _vp), ("bias_vals", _vp), ("bias_stride", _i64), ("mask", _vp),
@@ -262,14 +268,24 @@ class LogitsArgs(_Args):
 
 
 def _call(name, args, stream):
-    from . import _check, _stream, lib
-    import torch
+    if args._entry is None:                            # the entry point and its argument, looked up once
+        from . import lib
+        import torch
+        if args._name != name:
+            raise TypeError(f"{name}: got the arguments of {args._name}")
+        args._entry = name, getattr(lib(), name), ctypes.byref(args), torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    what, fn, ref, current, current_stream = args._entry
+    if what != name:
+        raise TypeError(f"{name}: got the arguments of {what}")
     dev = args._device
-    if dev is None or dev == torch.cuda.current_device():
-        _check(getattr(lib(), name)(ctypes.byref(args), _stream(stream)), name)
-    else:
+    if dev != current():
+        import torch
         with torch.cuda.device(dev):
-            _check(getattr(lib(), name)(ctypes.byref(args), _stream(stream)), name)
+            return _call(name, args, stream)
+    rc = fn(ref, current_stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream)
+    if rc:
+        from . import _check
+        _check(rc, name)
 
 
 def kv_append(args: AppendArgs, stream=None):
