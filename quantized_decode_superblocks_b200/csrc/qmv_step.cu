@@ -359,11 +359,14 @@ int logits_argmax(const qmv_logits *a, qmv_stream_t stream)
     p.idx = a->idx_out;
     p.keys = static_cast<unsigned long long *>(a->workspace);
     p.done = reinterpret_cast<unsigned *>(p.keys + a->n_rows);
-    p.slice = logits_slice(a->n_rows, a->vocab, di.sm_count);
+    const bool wide = (p.hist && p.hist_stride > 65535) || (p.bias_ids && p.bias_stride >= 65535);
+    p.slice = logits_slice(a->n_rows, a->vocab, di.sm_count, wide);
     const dim3 grid((unsigned)ceil_div(a->vocab, p.slice), (unsigned)a->n_rows);
-    static SmemCfg configured;
-    const size_t smem = p.hist || p.bias_ids ? (size_t)p.slice * sizeof(int2) : 0;
-    return finish(launch_with(logits_argmax_kernel, configured, p, grid, smem, reinterpret_cast<cudaStream_t>(stream), false, false, LG_THREADS));
+    static SmemCfg configured[2];
+    const size_t smem = logits_smem(p.slice, wide);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return finish(wide ? launch_with(logits_argmax_kernel<true>, configured[1], p, grid, smem, st, false, false, LG_THREADS)
+                       : launch_with(logits_argmax_kernel<false>, configured[0], p, grid, smem, st, false, false, LG_THREADS));
 }
 
 }  // extern "C"
