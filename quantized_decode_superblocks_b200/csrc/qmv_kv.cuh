@@ -10,9 +10,18 @@ namespace qmv {
 
 // -------------------------------------------------------------- append --
 // One CTA per (token, share of the heads): the token's cosines and sines once
-// in 64 bits, then one warp per head.  A few KB per token:
-// bound by launch and memory latency, not by bandwidth.
-constexpr int APP_THREADS = 256;
+// in 64 bits, then one warp per head, whose first head is loaded meanwhile.  A
+// few KB per token: bound by launch and memory latency, not by bandwidth.
+constexpr int APP_THREADS = 128, APP_CTAS = 4;     // CTAs on a SM
+
+// Sine and cosine of pos * f.  The angle is brought within one turn by k turns
+// taken away in two parts (Cody and Waite), exact to 2^-53 of a turn for any
+// 31-bit position, so that the library's function never takes its long path.
+__device__ __forceinline__ void rope_sincos(double pos, float f, double *s, double *c)
+{
+    const double a = pos * (double)f, k = rint(a * 0.15915494309189535);
+    sincos(fma(-k, 2.4492935982947064e-16, fma(-k, 6.283185307179586, a)), s, c);
+}
 
 struct AppendParams {
     uint8_t *k, *v, *ks, *vs;
@@ -28,7 +37,7 @@ struct AppendParams {
     int *err;
 };
 
-static __global__ void __launch_bounds__(APP_THREADS) kv_append_kernel(const __grid_constant__ AppendParams p)
+static __global__ void __launch_bounds__(APP_THREADS, APP_CTAS) kv_append_kernel(const __grid_constant__ AppendParams p)
 {
     __shared__ double s_cos[128], s_sin[128];
     __shared__ long long s_at;                     // the slot's first element, -1: nothing to store
@@ -45,24 +54,31 @@ static __global__ void __launch_bounds__(APP_THREADS) kv_append_kernel(const __g
         if (raw != len) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
         s_at = at;
     }
-    const double pos = p.pos ? __ldg(p.pos + tok) : slot;
-    for (int i = threadIdx.x; i < p.rope_dim / 2; i += APP_THREADS) sincos(pos * (double)__ldg(p.inv_freq + i), s_sin + i, s_cos + i);
-    __syncthreads();
-    const long long at = s_at;
     const int nb = (p.dim + 31) / 32, nq = p.q_out ? p.n_head : 0, heads = nq + 2 * p.n_kv;
-    const int half = p.rope_dim / 2;
-    for (int head = blockIdx.y * (APP_THREADS / 32) + warp; head < heads; head += gridDim.y * (APP_THREADS / 32)) {
+    const int half = p.rope_dim / 2, step = gridDim.y * (APP_THREADS / 32);
+    int head = blockIdx.y * (APP_THREADS / 32) + warp;
+    float y[8], z[8];                              // this lane's values and their partners
+    auto load = [&]() {
+        if (head >= heads) return;
         const bool is_q = head < nq, is_k = !is_q && head < nq + p.n_kv;
         const int h = is_q ? head : is_k ? head - nq : head - nq - p.n_kv;
         const float *x = is_q ? p.q_in + tok * p.q_stride : is_k ? p.k_in + tok * p.k_stride : p.v_in + tok * p.v_stride;
         x += (int64_t)h * p.dim;
-        float y[8], z[8];                          // this lane's values and their partners
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
             const int d = b * 32 + lane;
             y[b] = b < nb && d < p.dim ? x[d] : 0.f;
             z[b] = !is_q && !is_k ? 0.f : d < p.rope_dim ? x[p.rope_pairs ? d ^ 1 : d < half ? d + half : d - half] : 0.f;
         }
+    };
+    load();
+    const double pos = p.pos ? __ldg(p.pos + tok) : slot;
+    for (int i = threadIdx.x; i < half; i += APP_THREADS) rope_sincos(pos, __ldg(p.inv_freq + i), s_sin + i, s_cos + i);
+    __syncthreads();
+    const long long at = s_at;
+    for (; head < heads; head += step, load()) {
+        const bool is_q = head < nq, is_k = !is_q && head < nq + p.n_kv;
+        const int h = is_q ? head : is_k ? head - nq : head - nq - p.n_kv;
         __syncwarp();                              // q may be rotated in place: all is read before anything is written
 #pragma unroll
         for (int b = 0; b < 8; ++b) {

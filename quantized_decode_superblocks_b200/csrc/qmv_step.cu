@@ -246,7 +246,7 @@ int kv_append(const qmv_append *a, qmv_stream_t stream)
     p.err = di.err;
     const int tokens = a->n_seq * a->n_tok;
     const int heads = (a->q ? a->n_head : 0) + 2 * c.n_kv_head;
-    const int gy = (int)std::min<int64_t>(ceil_div(heads, APP_THREADS / 32), std::max(1, 4 * di.sm_count / tokens));
+    const int gy = (int)std::min<int64_t>(ceil_div(heads, APP_THREADS / 32), std::max(1, APP_CTAS * di.sm_count / tokens));
     kv_append_kernel<<<dim3((unsigned)tokens, (unsigned)gy), APP_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     return finish(cudaGetLastError());
 }
