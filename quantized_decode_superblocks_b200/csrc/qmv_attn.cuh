@@ -55,7 +55,12 @@ enum { KV_F16 = 0, KV_BF16 = 1, KV_Q8_0 = 2 };
 
 constexpr int ATT_NW = 4;                    // warps of a CTA
 constexpr int ATT_THREADS = ATT_NW * 32;
-constexpr int ATT_TILE = 16;                 // slots of a tile
+// Slots of a tile: 32 where its keys and values are short and registers allow, so
+// that a warp's work around a tile is spread over more of them.  Against 16: f16,
+// 64 wide, one token over 131071 slots 60 -> 54 us; Q8_0, 128 wide, one token for
+// 16 sequences 105 -> 88 us, but 16 rows of them 82 -> 112 us.
+__host__ __device__ constexpr int attn_tile(int type, int dp, int mb) { return dp <= 64 || (type == 2 && dp <= 128 && mb == 1) ? 32 : 16; }
+constexpr int ATT_MIN_TILE = 16, ATT_MAX_TILE = 32;
 // log2 of how far a weight may pass 1, and of the factor of the weights in f16
 // parts: together below 2^16, and the second keeps what an f16 part cuts off
 // (half a step of its subnormals) below 2^-34 of the reference.  bf16 parts
@@ -63,10 +68,12 @@ constexpr int ATT_TILE = 16;                 // slots of a tile
 __host__ __device__ constexpr float attn_slack(int type) { return type == 1 ? 12.f : 6.f; }
 constexpr float ATT_F16_SHIFT = 9.f;
 
-// 8-row blocks that one CTA takes at most: the outputs of 4 (2) of them fill half its registers
-__host__ __device__ constexpr int attn_max_mb(int dim) { return dim <= 128 ? 4 : 2; }
+// 8-row blocks that one CTA takes: up to 2.  (With 4, whose outputs and operands
+// leave no registers to overlap anything, 32 rows over 4096 slots of 4 sequences
+// take 74 us instead of 45 us in bf16 and 53 us instead of 43 us in Q8_0, 128 wide.)
+__host__ __device__ constexpr int attn_mb(int rows) { return rows <= 8 ? 1 : 2; }
 constexpr int ATT_MAX_SEQ = 1024;
-constexpr int ATT_MAX_CTAS = 320;            // bound for the workspace's parts
+constexpr int ATT_MAX_CTAS = 480;            // bound for the workspace's parts
 
 struct AttnParams {
     const uint8_t *k, *v, *ks, *vs;
@@ -84,7 +91,7 @@ struct AttnParams {
     float scale_log2, l_shift;                           // l counts 2^l_shift times the weights
     unsigned *counters;                                  // [ATT_MAX_CTAS], zero between calls
     float *part_ml, *part_o;                             // [2 * CTAs][8 mb][2], [..][dim]
-    float *raw, *stats;                                  // scores s [..][slot][row] and (m, l) of every row, for `score`
+    float *raw, *stats;                                  // for `score`: scores s [..][slot][row]; (m - l_shift, 1 / l or 0) of every row
     int64_t raw_stride;                                  // slots
     int32_t raw_rows;                                    // rows, made even
     int *err;
@@ -97,6 +104,7 @@ struct AttnSeq {
     int sink_tiles, base;  // tiles 0 .. sink_tiles - 1 start at slot 0, the others at slot base
     int n_tiles, n_steps;  // at least 1, so that every row gets written
 
+    template <int TILE>
     __device__ __forceinline__ void set(int n, const AttnParams &p)
     {
         len = n;
@@ -105,22 +113,24 @@ struct AttnSeq {
         if (p.window > 0) {
             lo = max(0, max(first, 0) - p.window + 1);
             sinks = min(p.n_sink, lo);
-            sink_tiles = (sinks + ATT_TILE - 1) / ATT_TILE;
-            base = lo / ATT_TILE * ATT_TILE;
-            if (sinks > 0 && sink_tiles * ATT_TILE >= base) sink_tiles = base = 0;   // the parts meet
+            sink_tiles = (sinks + TILE - 1) / TILE;
+            base = lo / TILE * TILE;
+            if (sinks > 0 && sink_tiles * TILE >= base) sink_tiles = base = 0;   // the parts meet
         }
-        n_tiles = max(1, sink_tiles + (len - base + ATT_TILE - 1) / ATT_TILE);
+        n_tiles = max(1, sink_tiles + (len - base + TILE - 1) / TILE);
         n_steps = (n_tiles + ATT_NW - 1) / ATT_NW;
     }
+    template <int TILE>
     __device__ __forceinline__ int slot0(int tile) const
     {
-        return tile < sink_tiles ? tile * ATT_TILE : base + (tile - sink_tiles) * ATT_TILE;
+        return tile < sink_tiles ? tile * TILE : base + (tile - sink_tiles) * TILE;
     }
     __device__ __forceinline__ bool seen(int j) const { return j < len && (j >= lo || j < sinks); }
-    // Slots j0 .. j0 + 15 are seen by every query (of several).
+    // Slots j0 .. j0 + TILE - 1 are seen by every query (of several).
+    template <int TILE>
     __device__ __forceinline__ bool by_all(int j0, const AttnParams &p) const
     {
-        return j0 + ATT_TILE - 1 <= first && (p.window == 0 || j0 > len - 1 - p.window || j0 + ATT_TILE <= p.n_sink);
+        return j0 + TILE - 1 <= first && (p.window == 0 || j0 > len - 1 - p.window || j0 + TILE <= p.n_sink);
     }
 };
 
@@ -256,16 +266,20 @@ __device__ __forceinline__ void i8_to_f16(uint32_t w, uint32_t &p0, uint32_t &p1
 // Shared-memory geometry of one instance: MB 8-row blocks of a DP-wide head.
 template <int TYPE, int DP, int MB>
 struct AttnGeom {
+    static constexpr int TILE = attn_tile(TYPE, DP, MB), SUB = TILE / 16;     // slots of a tile, and products of 16
+    static constexpr uint32_t ALL = 0xFFFFFFFFu >> (32 - TILE);
     static constexpr int EB = TYPE == KV_Q8_0 ? 1 : 2;           // bytes of a value
     static constexpr int PITCH = DP * EB;                        // bytes of a slot's k (or v)
     static constexpr int NCHUNK = PITCH / 16;
-    static constexpr int KV_BYTES = ATT_TILE * PITCH;            // a tile's k (or v)
+    static constexpr int KV_BYTES = TILE * PITCH;            // a tile's k (or v)
     static constexpr int SC_PITCH = DP / 32 * 2;                 // a slot's scales
-    static constexpr int SC_BYTES = TYPE == KV_Q8_0 ? ATT_TILE * SC_PITCH : 0;
+    static constexpr int SC_BYTES = TYPE == KV_Q8_0 ? TILE * SC_PITCH : 0;
     static constexpr int STAGE = 2 * (KV_BYTES + SC_BYTES);      // one warp's stage: k | v | k scales | v scales
     static constexpr int ROWS = 8 * MB;
-    // Stages: about 96 KB of ring a CTA, two CTAs a SM (one where a stage is 16 KB).
-    static constexpr int NST = STAGE >= 8 * 1024 ? 3 : STAGE >= 4 * 1024 ? 5 : 8;
+    // Stages: about 96 KB of ring a CTA, two CTAs a SM (one where a stage is 16
+    // KB); 64 KB and three CTAs for 8 narrow rows, which have the registers for it.
+    static constexpr bool NARROW = MB == 1 && DP <= 64;
+    static constexpr int NST = NARROW ? (TYPE == KV_Q8_0 ? 4 : 2) : STAGE >= 8 * 1024 ? 3 : 5;
     static constexpr int RING = ATT_NW * NST * STAGE;
     static constexpr int NPQ = TYPE == KV_BF16 ? 3 : 2;          // parts of q
     static constexpr int NPP = TYPE == KV_BF16 ? 3 : 2;          // parts of the weights
@@ -275,25 +289,23 @@ struct AttnGeom {
     static constexpr int OPITCH = DP + 4;                        // floats: a store's rows in different banks
     static_assert(ATT_NW * ROWS * OPITCH * 4 <= RING, "the warps' outputs are joined in the ring");
     static constexpr int SMEM = RING + Q_BYTES;
-    static constexpr int CTAS = SMEM <= 110 * 1024 ? 2 : 1;      // on a SM
+    static constexpr int CTAS = NARROW ? 3 : SMEM <= 110 * 1024 ? 2 : 1;          // on a SM
+    static_assert(!NARROW || SMEM <= 70 * 1024, "three CTAs' shared memory");
     static_assert(SMEM <= 222 * 1024, "one CTA's shared memory");
     // 16-byte chunk c of slot r, so that 8 slots' chunks fall in different banks
-    static __device__ __forceinline__ uint32_t at(int r, int c)
-    {
-        const int x = NCHUNK >= 8 ? (r & 7) : ((r >> 1) & 3);
-        return (uint32_t)(r * PITCH + ((c ^ x) << 4));
-    }
+    static __device__ __forceinline__ int mix(int r) { return NCHUNK >= 8 ? (r & 7) : ((r >> 1) & 3); }
+    static __device__ __forceinline__ uint32_t at(int r, int c) { return (uint32_t)(r * PITCH + ((c ^ mix(r)) << 4)); }
 };
 
 template <int TYPE, int DP, int MB>
 __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) attn_decode_kernel(const __grid_constant__ AttnParams p)
 {
     using G = AttnGeom<TYPE, DP, MB>;
-    constexpr int NW = ATT_NW, NT = ATT_THREADS, NPQ = G::NPQ, NPP = G::NPP, QW = G::QW;
+    constexpr int NW = ATT_NW, NT = ATT_THREADS, NPQ = G::NPQ, NPP = G::NPP, QW = G::QW, TILE = G::TILE, SUB = G::SUB;
     constexpr bool PBF = TYPE == KV_BF16;                        // type of the second product's parts
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_pref[ATT_MAX_SEQ + 1];                      // steps of one head before each sequence
-    __shared__ int s_warp[NW];
+    __shared__ int4 s_warp[NW];
     __shared__ float s_m[NW][G::ROWS], s_l[NW][G::ROWS];
     __shared__ float s_lr[G::ROWS], s_sf[G::ROWS];
     __shared__ int s_at[G::ROWS];                                // the slot of each row's query, -1 for rows past the end
@@ -303,45 +315,83 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
     const int g = lane >> 2, c4 = lane & 3;
     const uint32_t ring0 = smem_addr(smem);
     const int units = p.n_rb * p.n_kv;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // attn_score_kernel, if it follows, waits for this one's end
 
-    // ---- where this CTA's steps lie: prefix sum of the sequences' steps
-    {
+    // ---- where this CTA's steps lie.  Every CTA gets `share` steps; where a little
+    // more than the equal share lets each CTA stay within one segment (sequence, row
+    // block, head), segments are padded to whole shares: a CTA then neither drains
+    // its ring nor joins twice.
+    auto steps_of = [&](int s) {
+        AttnSeq q;
+        q.set<TILE>(attn_len(p, s), p);
+        return q.n_steps;
+    };
+    auto prefix = [&](auto &&length) {                                    // s_pref[s] = sum of the lengths before sequence s
         int run = 0;
         for (int s0 = 0; s0 < p.n_seq; s0 += NT) {
-            const int s = s0 + tid;
-            int n = 0;
-            if (s < p.n_seq) {
-                const int raw = __ldg(p.kv_len + s);
-                if ((raw < 0 || raw > p.max_len) && blockIdx.x == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
-                AttnSeq q;
-                q.set(min(max(raw, 0), p.max_len), p);
-                n = q.n_steps;
-            }
+            const int s = s0 + tid, n = s < p.n_seq ? length(s) : 0;
             int x = n;
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
                 if (lane >= o) x += y;
             }
-            if (lane == 31) s_warp[warp] = x;
+            if (lane == 31) s_warp[warp].x = x;
             __syncthreads();
-            int before = run, all = run;
+            int before = run, upto = run;
             for (int w = 0; w < NW; ++w) {
-                if (w < warp) before += s_warp[w];
-                all += s_warp[w];
+                if (w < warp) before += s_warp[w].x;
+                upto += s_warp[w].x;
             }
             if (s < p.n_seq) s_pref[s] = before + x - n;
-            run = all;
-            __syncthreads();
+            run = upto;
+            if (s0 + NT < p.n_seq) __syncthreads();
         }
         if (tid == 0) s_pref[p.n_seq] = run;
+        __syncthreads();
+        return (unsigned)run * (unsigned)units;                           // below 2^31
+    };
+    unsigned total = prefix([&](int s) {
+        const int raw = __ldg(p.kv_len + s);
+        if ((raw < 0 || raw > p.max_len) && blockIdx.x == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
+        return steps_of(s);
+    });
+    int share = (int)((total + gridDim.x - 1) / gridDim.x);
+    bool padded = false;
+    if (share > 1 && p.n_seq * units <= (int)gridDim.x) {
+        int4 n = make_int4(0, 0, 0, 0);                                   // CTAs at shares of share .. share + 3
+        for (int s = tid; s < p.n_seq; s += NT) {
+            const unsigned k = (unsigned)steps_of(s) - 1u;
+            n.x += k / (unsigned)share + 1u;
+            n.y += k / (unsigned)(share + 1) + 1u;
+            n.z += k / (unsigned)(share + 2) + 1u;
+            n.w += k / (unsigned)(share + 3) + 1u;
+        }
+        n.x = __reduce_add_sync(0xFFFFFFFFu, n.x);
+        n.y = __reduce_add_sync(0xFFFFFFFFu, n.y);
+        n.z = __reduce_add_sync(0xFFFFFFFFu, n.z);
+        n.w = __reduce_add_sync(0xFFFFFFFFu, n.w);
+        if (lane == 0) s_warp[warp] = n;
+        __syncthreads();
+        n = make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            n.x += s_warp[w].x; n.y += s_warp[w].y; n.z += s_warp[w].z; n.w += s_warp[w].w;
+        }
+        __syncthreads();
+        const int most = (int)gridDim.x, more = n.x * units <= most ? 0 : n.y * units <= most ? 1 : n.z * units <= most ? 2 : n.w * units <= most ? 3 : 4;
+        padded = more < 4 && more <= share / 8 + 1;
+        if (padded) share += more;
     }
-    __syncthreads();
-    const unsigned total = (unsigned)s_pref[p.n_seq] * (unsigned)units, share = (total + gridDim.x - 1) / gridDim.x;    // below 2^31
-    const int x0 = (int)min(total, share * blockIdx.x), x1 = (int)min(total, x0 + share);
+    auto length_of = [&](int n) { return padded ? (int)((unsigned)(n + share - 1) / (unsigned)share) * share : n; };
+    if (padded) total = prefix([&](int s) { return length_of(steps_of(s)); });
+    const int x0 = (int)min(total, (unsigned)share * blockIdx.x), x1 = (int)min(total, (unsigned)x0 + share);
 
     const int nchunk = p.dim * G::EB / 16;
     const uint32_t my_ring = ring0 + (uint32_t)(warp * G::NST * G::STAGE);
-    const bool one_page = p.page_size % ATT_TILE == 0;           // a tile never leaves its page
+    const bool one_page = p.page_size % 16 == 0;                 // 16 slots never leave their page
+    constexpr int LPR = G::NCHUNK < 32 ? G::NCHUNK : 32, RPI = 32 / LPR;         // copies: lanes of a slot, slots of a pass
+    const int ch = lane % LPR;
+    const int64_t lane_at = (lane / LPR) * p.slot_stride * G::EB + ch * 16, pass_step = RPI * p.slot_stride * G::EB;
     const uint32_t k_row = ((lane >> 3) & 1) * 8 + (lane & 7), k_chunk = lane >> 4;       // ldmatrix addresses: K
     const uint32_t v_row = TYPE == KV_Q8_0 ? k_row : (lane >> 4) * 8 + (lane & 7);        // and V
     const uint32_t v_chunk = TYPE == KV_Q8_0 ? k_chunk : (lane >> 3) & 1;
@@ -358,23 +408,42 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
             }
         }
         AttnSeq sq;
-        sq.set(attn_len(p, s), p);
+        sq.set<TILE>(attn_len(p, s), p);
         const int seq0 = s_pref[s] * units;
-        const int unit = (int)((unsigned)(x - seq0) / (unsigned)sq.n_steps);
+        const int length = length_of(sq.n_steps), unit = (int)((unsigned)(x - seq0) / (unsigned)length);
         const int h = p.n_rb == 1 ? unit : unit / p.n_rb, rb = unit - h * p.n_rb;        // a head's row blocks follow each other: the cache is in L2
-        const int seg0 = seq0 + unit * sq.n_steps, seg1 = seg0 + sq.n_steps;
+        const int seg0 = seq0 + unit * length, seg1 = seg0 + length;
         const int row0 = rb * G::ROWS;
         const int tile0 = (x - seg0) * NW + warp;                         // this warp's first tile
-        const int k0 = x - seg0, k1 = min(seg1, x1) - seg0;               // steps of the segment
+        const int k0 = x - seg0, k1 = min(min(seg1, x1) - seg0, sq.n_steps);          // steps of the segment
         const int n_steps = max(0, min(k1, (sq.n_tiles - warp + NW - 1) / NW) - k0);      // this warp has a tile in
         const int32_t *tab = p.table + (int64_t)s * p.table_stride;
-        x += k1 - k0;
+        x = min(seg1, x1);
+
+        // ---- 8 narrow rows' q before the copies, behind which its loads would wait
+        float qraw[G::QREG ? DP / 16 : 1][4];
+        auto q_row = [&](int row) {
+            const int tok = row < p.rows ? row / p.group : 0;
+            return p.q + (int64_t)(s * p.n_tok + tok) * p.q_stride + (int64_t)(h * p.group + (row < p.rows ? row - tok * p.group : 0)) * p.dim;
+        };
+        auto q_load4 = [&](const float *x, bool row_ok, int ks, float (&f)[4]) {
+            const int d0 = ks * 16 + (TYPE == KV_Q8_0 ? 4 * c4 : 2 * c4), d1 = TYPE == KV_Q8_0 ? d0 + 2 : d0 + 8;
+            const bool ok = row_ok && ks * 16 < p.dim;
+            const float2 a = ok ? __ldg(reinterpret_cast<const float2 *>(x + d0)) : make_float2(0.f, 0.f);
+            const float2 b = ok ? __ldg(reinterpret_cast<const float2 *>(x + d1)) : make_float2(0.f, 0.f);
+            f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+        };
+        if constexpr (G::QREG) {
+            const float *x = q_row(row0 + g);
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) q_load4(x, row0 + g < p.rows, ks, qraw[ks]);
+        }
 
         // ---- the ring: page entries one step ahead of the copies
         auto fetch_page = [&](int step) {
             int pg = -1;
             if (step < n_steps) {
-                const int j = sq.slot0(tile0 + step * NW) + (one_page ? 0 : lane & (ATT_TILE - 1));
+                const int j = sq.slot0<TILE>(tile0 + step * NW) + (one_page ? lane & (TILE - 16) : lane & (TILE - 1));
                 if (one_page ? j < sq.len : sq.seen(j)) {
                     pg = __ldg(tab + (p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size));
                 }
@@ -384,38 +453,55 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
         auto issue = [&](int step, int st, int pg) {
             if (step < n_steps) {
                 const uint32_t dst = my_ring + (uint32_t)(st * G::STAGE);
-                const int j0 = sq.slot0(tile0 + step * NW), j = j0 + (one_page ? 0 : lane & (ATT_TILE - 1));
+                const int j0 = sq.slot0<TILE>(tile0 + step * NW), j = j0 + (one_page ? lane & (TILE - 16) : lane & (TILE - 1));
                 const int o = p.page_shift >= 0 ? j & (p.page_size - 1) : j % p.page_size;
                 const long long e = pg * p.page_stride + h * p.head_stride + o * p.slot_stride;
-                const bool bad = pg < 0 || pg >= p.n_pages, want = lane < ATT_TILE && sq.seen(j0 + lane);
+                const bool bad = pg < 0 || pg >= p.n_pages, want = lane < TILE && sq.seen(j0 + lane);
                 const uint32_t use = __ballot_sync(0xFFFFFFFFu, want && !bad);
                 if (want && bad) atomicOr(p.err, 8 /* QMV_DEVERR_PAGE_ID */);
                 if (lane == 0) s_mask[warp][st] = use;
-                constexpr int LPR = G::NCHUNK < 32 ? G::NCHUNK : 32;      // lanes of a row
-                constexpr int RPI = 32 / LPR;                             // rows of a pass
-                const int ch = lane % LPR;
-                // rows' addresses: from the tile's when it lies in one page, else from the lane of the row
-                const int64_t e1 = (e + (lane / LPR) * p.slot_stride) * G::EB + ch * 16, step_b = RPI * p.slot_stride * G::EB;
+                // rows' addresses: from the first of their 16 where those lie in one page, else from the lane of the row
+                static_assert(RPI <= 16, "a pass's rows lie in one group of 16");
+                const uint32_t to = dst + (uint32_t)(lane / LPR * G::PITCH);
+                if (one_page && use == G::ALL && nchunk == G::NCHUNK) {
 #pragma unroll
-                for (int i = 0; i < ATT_TILE / RPI; ++i) {
-                    const int r = i * RPI + lane / LPR;
-                    const bool ok = ((use >> r) & 1u) && ch < nchunk;
-                    int64_t at = e1 + i * step_b;
-                    if (!one_page) at = __shfl_sync(0xFFFFFFFFu, e, r) * G::EB + ch * 16;
-                    if (!ok) at = 0;
-                    cp_async16(dst + G::at(r, ch), p.k + at, ok ? 16u : 0u);
-                    cp_async16(dst + G::KV_BYTES + G::at(r, ch), p.v + at, ok ? 16u : 0u);
+                    for (int u = 0; u < SUB; ++u) {
+                        const int64_t at = (SUB == 1 ? e : __shfl_sync(0xFFFFFFFFu, e, 16 * u)) * G::EB + lane_at;
+                        const uint8_t *k = p.k + at, *v = p.v + at;
+#pragma unroll
+                        for (int i = 0; i < 16 / RPI; ++i) {
+                            const uint32_t x = to + (uint32_t)((16 * u + i * RPI) * G::PITCH) + ((uint32_t)(ch ^ G::mix(i * RPI + lane / LPR)) << 4);
+                            cp_async16(x, k, 16u);
+                            cp_async16(x + G::KV_BYTES, v, 16u);
+                            k += pass_step;
+                            v += pass_step;
+                        }
+                    }
+                } else {
+                    int64_t e16[SUB];
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) e16[u] = SUB == 1 ? e : __shfl_sync(0xFFFFFFFFu, e, 16 * u);
+#pragma unroll
+                    for (int i = 0; i < TILE / RPI; ++i) {
+                        const int r = i * RPI + lane / LPR;
+                        const bool ok = ((use >> r) & 1u) && ch < nchunk;
+                        int64_t at = (e16[i * RPI / 16] + (r & 15) * p.slot_stride) * G::EB + ch * 16;
+                        if (!one_page) at = __shfl_sync(0xFFFFFFFFu, e, r) * G::EB + ch * 16;
+                        if (!ok) at = 0;
+                        cp_async16(dst + G::at(r, ch), p.k + at, ok ? 16u : 0u);
+                        cp_async16(dst + G::KV_BYTES + G::at(r, ch), p.v + at, ok ? 16u : 0u);
+                    }
                 }
                 if constexpr (TYPE == KV_Q8_0) {
                     constexpr int WPR = DP / 64;                          // 4-byte words of a slot's scales
                     const int nw = p.dim / 64;
 #pragma unroll
-                    for (int i0 = 0; i0 < ATT_TILE * WPR; i0 += 32) {
+                    for (int i0 = 0; i0 < TILE * WPR; i0 += 32) {
                         const int r = (i0 + lane) / WPR, w = (i0 + lane) % WPR;
-                        const long long er = one_page ? e + r * p.slot_stride : __shfl_sync(0xFFFFFFFFu, e, r & 15);
-                        const bool ok = r < ATT_TILE && ((use >> r) & 1u) && w < nw;
-                        const int64_t at = ok ? er / 16 + w * 4 : 0;
-                        if (r < ATT_TILE) {
+                        const long long from = __shfl_sync(0xFFFFFFFFu, e, one_page ? r & (TILE - 16) : r & (TILE - 1));
+                        const bool ok = r < TILE && ((use >> r) & 1u) && w < nw;
+                        const int64_t at = ok ? (one_page ? from + (r & 15) * p.slot_stride : from) / 16 + w * 4 : 0;
+                        if (r < TILE) {
                             cp_async4(dst + 2 * G::KV_BYTES + r * G::SC_PITCH + w * 4, p.ks + at, ok ? 4u : 0u);
                             cp_async4(dst + 2 * G::KV_BYTES + G::SC_BYTES + r * G::SC_PITCH + w * 4, p.vs + at, ok ? 4u : 0u);
                         }
@@ -441,15 +527,13 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
         const uint32_t qs0 = ring0 + G::RING;
         auto q_block = [&](int nb, auto &&put) {                          // returns the row's factor of the scores
             const int row = row0 + nb * 8 + g;
-            const bool row_ok = row < p.rows;
-            const int tok = row_ok ? row / p.group : 0;
-            const float *x = p.q + (int64_t)(s * p.n_tok + tok) * p.q_stride + (int64_t)(h * p.group + (row_ok ? row - tok * p.group : 0)) * p.dim;
+            const float *x = q_row(row);
             auto load4 = [&](int ks, float (&f)[4]) {
-                const int d0 = ks * 16 + (TYPE == KV_Q8_0 ? 4 * c4 : 2 * c4), d1 = TYPE == KV_Q8_0 ? d0 + 2 : d0 + 8;
-                const bool ok = row_ok && ks * 16 < p.dim;
-                const float2 a = ok ? __ldg(reinterpret_cast<const float2 *>(x + d0)) : make_float2(0.f, 0.f);
-                const float2 b = ok ? __ldg(reinterpret_cast<const float2 *>(x + d1)) : make_float2(0.f, 0.f);
-                f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+                if constexpr (G::QREG) {
+                    f[0] = qraw[ks][0]; f[1] = qraw[ks][1]; f[2] = qraw[ks][2]; f[3] = qraw[ks][3];
+                } else {
+                    q_load4(x, row < p.rows, ks, f);
+                }
             };
             float qmul = 1.f, sf = p.scale_log2;
             if constexpr (TYPE != KV_BF16) {
@@ -539,88 +623,104 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
             __syncwarp();
             issue(step + G::NST - 1, st == 0 ? G::NST - 1 : st - 1, pg_next);
             pg_next = fetch_page(step + G::NST);
-            const int j0 = sq.slot0(tile0 + step * NW);
+            const int j0 = sq.slot0<TILE>(tile0 + step * NW);
             const uint32_t buf = my_ring + (uint32_t)(st * G::STAGE), use = s_mask[warp][st];
             if (++st == G::NST) st = 0;
             // -- scores: this lane's are slots g (values 0, 1) and g + 8 (2, 3), rows 2 c4 and 2 c4 + 1 of every block
-            float sc[MB][4];
+            float sc[MB][SUB][4];
             if constexpr (TYPE == KV_Q8_0) {
 #pragma unroll
-                for (int nb = 0; nb < MB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+                for (int nb = 0; nb < MB; ++nb)
 #pragma unroll
-                for (int b = 0; b < DP / 32; ++b) {
-                    uint32_t r[4], a[2][4];
-                    ldsm4(r, buf + G::at(k_row, 2 * b + k_chunk));
+                    for (int u = 0; u < SUB; ++u) sc[nb][u][0] = sc[nb][u][1] = sc[nb][u][2] = sc[nb][u][3] = 0.f;
 #pragma unroll
-                    for (int k2 = 0; k2 < 2; ++k2) {
-                        i8_to_f16(r[2 * k2], a[k2][0], a[k2][2]);
-                        i8_to_f16(r[2 * k2 + 1], a[k2][1], a[k2][3]);
+                for (int b = 0; b < DP / 32; ++b)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        uint32_t r[4], a[2][4];
+                        ldsm4(r, buf + G::at(16 * u + k_row, 2 * b + k_chunk));
+#pragma unroll
+                        for (int k2 = 0; k2 < 2; ++k2) {
+                            i8_to_f16(r[2 * k2], a[k2][0], a[k2][2]);
+                            i8_to_f16(r[2 * k2 + 1], a[k2][1], a[k2][3]);
+                        }
+                        const uint32_t sa = buf + 2 * G::KV_BYTES + 2 * b + (16 * u + g) * G::SC_PITCH;
+                        const float d0 = half_bits_to_float(lds_u16(sa)), d1 = half_bits_to_float(lds_u16(sa + 8 * G::SC_PITCH));
+#pragma unroll
+                        for (int nb = 0; nb < MB; ++nb) {
+                            float hi[4], lo[4];
+                            uint32_t q[QW];
+                            q_frag(nb, 2 * b, q);
+                            mma_16_0<false>(hi, a[0], q[0], q[1]);
+                            mma_16_0<false>(lo, a[0], q[2], q[3]);
+                            q_frag(nb, 2 * b + 1, q);
+                            mma_16<false>(hi, a[1], q[0], q[1]);
+                            mma_16<false>(lo, a[1], q[2], q[3]);
+                            add2(hi[0], hi[1], lo[0], lo[1]);
+                            add2(hi[2], hi[3], lo[2], lo[3]);
+                            fma2(sc[nb][u][0], sc[nb][u][1], hi[0], hi[1], d0);
+                            fma2(sc[nb][u][2], sc[nb][u][3], hi[2], hi[3], d1);
+                        }
                     }
-                    const uint32_t sa = buf + 2 * G::KV_BYTES + 2 * b;
-                    const float d0 = half_bits_to_float(lds_u16(sa + g * G::SC_PITCH)), d1 = half_bits_to_float(lds_u16(sa + (g + 8) * G::SC_PITCH));
-#pragma unroll
-                    for (int nb = 0; nb < MB; ++nb) {
-                        float hi[4], lo[4];
-                        uint32_t q[QW];
-                        q_frag(nb, 2 * b, q);
-                        mma_16_0<false>(hi, a[0], q[0], q[1]);
-                        mma_16_0<false>(lo, a[0], q[2], q[3]);
-                        q_frag(nb, 2 * b + 1, q);
-                        mma_16<false>(hi, a[1], q[0], q[1]);
-                        mma_16<false>(lo, a[1], q[2], q[3]);
-                        add2(hi[0], hi[1], lo[0], lo[1]);
-                        add2(hi[2], hi[3], lo[2], lo[3]);
-                        fma2(sc[nb][0], sc[nb][1], hi[0], hi[1], d0);
-                        fma2(sc[nb][2], sc[nb][3], hi[2], hi[3], d1);
-                    }
-                }
             } else {
-                constexpr int PAR = MB == 1 ? 2 : 1;                      // chains per part: their sums wait on the one before
-                float a[MB][NPQ][PAR][4];
+                constexpr int PAR = MB * SUB == 1 ? 2 : 1;                // chains per part: their sums wait on the one before
+                float a[MB][SUB][NPQ][PAR][4];
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
-                    uint32_t r[4];
-                    ldsm4(r, buf + G::at(k_row, 2 * ks + k_chunk));
+                    uint32_t r[SUB][4];
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) ldsm4(r[u], buf + G::at(16 * u + k_row, 2 * ks + k_chunk));
 #pragma unroll
                     for (int nb = 0; nb < MB; ++nb) {
                         uint32_t q[QW];
                         q_frag(nb, ks, q);
 #pragma unroll
-                        for (int i = 0; i < NPQ; ++i) {
-                            if (ks < PAR) mma_16_0<TYPE == KV_BF16>(a[nb][i][ks % PAR], r, q[2 * i], q[2 * i + 1]);
-                            else mma_16<TYPE == KV_BF16>(a[nb][i][ks % PAR], r, q[2 * i], q[2 * i + 1]);
-                        }
+                        for (int i = 0; i < NPQ; ++i)
+#pragma unroll
+                            for (int u = 0; u < SUB; ++u) {
+                                if (ks < PAR) mma_16_0<TYPE == KV_BF16>(a[nb][u][i][ks % PAR], r[u], q[2 * i], q[2 * i + 1]);
+                                else mma_16<TYPE == KV_BF16>(a[nb][u][i][ks % PAR], r[u], q[2 * i], q[2 * i + 1]);
+                            }
                     }
                 }
 #pragma unroll
                 for (int nb = 0; nb < MB; ++nb)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float t = 0.f;
+                    for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                        for (int i = NPQ - 1; i >= 0; --i) t += PAR == 2 ? a[nb][i][0][e] + a[nb][i][PAR - 1][e] : a[nb][i][0][e];
-                        sc[nb][e] = t;
-                    }
+                        for (int e = 0; e < 4; ++e) {
+                            float t = 0.f;
+#pragma unroll
+                            for (int i = NPQ - 1; i >= 0; --i) t += PAR == 2 ? a[nb][u][i][0][e] + a[nb][u][i][PAR - 1][e] : a[nb][u][i][0][e];
+                            sc[nb][u][e] = t;
+                        }
             }
 #pragma unroll
             for (int nb = 0; nb < MB; ++nb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nb][e] *= sf[nb][e & 1];
-            const bool mixed = p.n_tok > 1 && (use != 0xFFFFu || !sq.by_all(j0, p));
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[nb][u][e] *= sf[nb][e & 1];
+            const bool mixed = p.n_tok > 1 && (use != G::ALL || !sq.by_all<TILE>(j0, p));
             if (mixed) {
 #pragma unroll
                 for (int nb = 0; nb < MB; ++nb)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int jj = g + (e >> 1) * 8;
-                        if (!((use >> jj) & 1u) || !attn_sees(p, s_at[nb * 8 + 2 * c4 + (e & 1)], j0 + jj)) sc[nb][e] = -INFINITY;
-                    }
-            } else if (use != 0xFFFFu) {                                  // one query: what it sees was loaded
-                const bool u0 = (use >> g) & 1u, u1 = (use >> (g + 8)) & 1u;
+                    for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                for (int nb = 0; nb < MB; ++nb) {
-                    if (!u0) sc[nb][0] = sc[nb][1] = -INFINITY;
-                    if (!u1) sc[nb][2] = sc[nb][3] = -INFINITY;
+                        for (int e = 0; e < 4; ++e) {
+                            const int jj = 16 * u + g + (e >> 1) * 8;
+                            if (!((use >> jj) & 1u) || !attn_sees(p, s_at[nb * 8 + 2 * c4 + (e & 1)], j0 + jj)) sc[nb][u][e] = -INFINITY;
+                        }
+            } else if (use != G::ALL) {                                   // one query: what it sees was loaded
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    const bool u0 = (use >> (16 * u + g)) & 1u, u1 = (use >> (16 * u + g + 8)) & 1u;
+#pragma unroll
+                    for (int nb = 0; nb < MB; ++nb) {
+                        if (!u0) sc[nb][u][0] = sc[nb][u][1] = -INFINITY;
+                        if (!u1) sc[nb][u][2] = sc[nb][u][3] = -INFINITY;
+                    }
                 }
             }
             if (p.score) {
@@ -628,27 +728,36 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
 #pragma unroll
                 for (int nb = 0; nb < MB; ++nb)
                     if (row0 + nb * 8 + 2 * c4 < p.raw_rows) {
-                        *reinterpret_cast<float2 *>(raw + nb * 8) = make_float2(sc[nb][0], sc[nb][1]);
-                        *reinterpret_cast<float2 *>(raw + nb * 8 + 8 * (int64_t)p.raw_rows) = make_float2(sc[nb][2], sc[nb][3]);
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) {
+                            *reinterpret_cast<float2 *>(raw + nb * 8 + 16 * u * (int64_t)p.raw_rows) = make_float2(sc[nb][u][0], sc[nb][u][1]);
+                            *reinterpret_cast<float2 *>(raw + nb * 8 + (16 * u + 8) * (int64_t)p.raw_rows) = make_float2(sc[nb][u][2], sc[nb][u][3]);
+                        }
                     }
             }
             // -- the running maximum: moved only when a score is well above it
+            float mx[MB][2];
             bool up = false;
 #pragma unroll
             for (int nb = 0; nb < MB; ++nb)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) up |= fmaxf(sc[nb][e], sc[nb][e + 2]) > m[nb][e] + attn_slack(TYPE);
+                for (int e = 0; e < 2; ++e) {
+                    mx[nb][e] = fmaxf(sc[nb][0][e], sc[nb][0][e + 2]);
+#pragma unroll
+                    for (int u = 1; u < SUB; ++u) mx[nb][e] = fmaxf(mx[nb][e], fmaxf(sc[nb][u][e], sc[nb][u][e + 2]));
+                    up |= mx[nb][e] > m[nb][e] + attn_slack(TYPE);
+                }
             if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
                 for (int nb = 0; nb < MB; ++nb) {
                     float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(sc[nb][e], sc[nb][e + 2]);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-                        const float mn = fmaxf(m[nb][e], mx);
+                        float top = mx[nb][e];
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                        const float mn = fmaxf(m[nb][e], top);
                         f[e] = m[nb][e] == mn ? 1.f : ex2(m[nb][e] - mn);         // m = -inf: 0
                         m[nb][e] = mn;
                         l[nb][e] *= f[e];
@@ -666,90 +775,115 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float mref = (m[nb][e] == -INFINITY ? 0.f : m[nb][e]) - p.l_shift;
-                    sc[nb][e] = ex2(sc[nb][e] - mref);
-                    sc[nb][e + 2] = ex2(sc[nb][e + 2] - mref);
-                    l[nb][e] += sc[nb][e] + sc[nb][e + 2];
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        sc[nb][u][e] = ex2(sc[nb][u][e] - mref);
+                        sc[nb][u][e + 2] = ex2(sc[nb][u][e + 2] - mref);
+                        l[nb][e] += sc[nb][u][e] + sc[nb][u][e + 2];
+                    }
                 }
             // -- output += values x weights
             const uint32_t va = buf + G::KV_BYTES;
             if constexpr (TYPE == KV_Q8_0) {
                 // weights transposed to lane (row g, slots 2 c4, 2 c4 + 1 and + 8) as halves of 16 bits, then scaled per block of 32
-                float pw[MB][4];
+                float pw[MB][SUB][4];
 #pragma unroll
                 for (int nb = 0; nb < MB; ++nb)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t u0 = __float_as_uint(sc[nb][2 * i]), u1 = __float_as_uint(sc[nb][2 * i + 1]);
-                        const uint32_t hi = movm_t(__byte_perm(u0, u1, 0x7632)), lo = movm_t(__byte_perm(u0, u1, 0x5410));
-                        pw[nb][2 * i] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
-                        pw[nb][2 * i + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
-                    }
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t u0 = __float_as_uint(sc[nb][u][2 * i]), u1 = __float_as_uint(sc[nb][u][2 * i + 1]);
+                            const uint32_t hi = movm_t(__byte_perm(u0, u1, 0x7632)), lo = movm_t(__byte_perm(u0, u1, 0x5410));
+                            pw[nb][u][2 * i] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
+                            pw[nb][u][2 * i + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+                        }
 #pragma unroll
                 for (int b = 0; b < DP / 32; ++b) {
-                    uint32_t r[4];
-                    ldsm4t(r, va + G::at(v_row, 2 * b + v_chunk));
                     const uint32_t sa = buf + 2 * G::KV_BYTES + G::SC_BYTES + 2 * b;
-                    float d[4];
+                    float d[SUB][4], dm = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        d[i] = half_bits_to_float(lds_u16(sa + (2 * c4 + (i & 1) + (i >> 1) * 8) * G::SC_PITCH));
-                        if (mixed && !(fabsf(d[i]) < INFINITY)) d[i] = 0.f;       // NaN of a slot that this row may not see: its weight is 0
-                    }
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            d[u][i] = half_bits_to_float(lds_u16(sa + (16 * u + 2 * c4 + (i & 1) + (i >> 1) * 8) * G::SC_PITCH));
+                            if (mixed && !(fabsf(d[u][i]) < INFINITY)) d[u][i] = 0.f;       // NaN of a slot that this row may not see: its weight is 0
+                            dm = fmaxf(dm, fabsf(d[u][i]));
+                        }
                     // the scales over a power of two at least the largest of them: their products with the weights stay in f16
-                    float dm = fmaxf(fmaxf(fabsf(d[0]), fabsf(d[1])), fmaxf(fabsf(d[2]), fabsf(d[3])));
                     dm = fmaxf(dm, __shfl_xor_sync(0xFFFFFFFFu, dm, 1));
                     dm = fmaxf(dm, __shfl_xor_sync(0xFFFFFFFFu, dm, 2));
                     const uint32_t ex = min(__float_as_uint(dm) >> 23, 200u);
                     const float down = __uint_as_float((253u - ex) << 23), back = __uint_as_float((ex + 1u) << 23);
-                    mul2(d[0], d[1], down, down);
-                    mul2(d[2], d[3], down, down);
-                    uint32_t a[2][4];
+                    uint32_t a[SUB][2][4];
 #pragma unroll
-                    for (int k2 = 0; k2 < 2; ++k2) {                      // rows g and g + 8: dims 2 g and 2 g + 1 of 16
-                        i8_to_f16<0x4240, 0x4341>(r[2 * k2], a[k2][0], a[k2][1]);
-                        i8_to_f16<0x4240, 0x4341>(r[2 * k2 + 1], a[k2][2], a[k2][3]);
+                    for (int u = 0; u < SUB; ++u) {
+                        mul2(d[u][0], d[u][1], down, down);
+                        mul2(d[u][2], d[u][3], down, down);
+                        uint32_t r[4];
+                        ldsm4t(r, va + G::at(16 * u + v_row, 2 * b + v_chunk));
+#pragma unroll
+                        for (int k2 = 0; k2 < 2; ++k2) {                  // rows g and g + 8: dims 2 g and 2 g + 1 of 16
+                            i8_to_f16<0x4240, 0x4341>(r[2 * k2], a[u][k2][0], a[u][k2][1]);
+                            i8_to_f16<0x4240, 0x4341>(r[2 * k2 + 1], a[u][k2][2], a[u][k2][3]);
+                        }
                     }
 #pragma unroll
                     for (int nb = 0; nb < MB; ++nb) {
-                        float pd[4] = {pw[nb][0], pw[nb][1], pw[nb][2], pw[nb][3]};
-                        mul2(pd[0], pd[1], d[0], d[1]);
-                        mul2(pd[2], pd[3], d[2], d[3]);
-                        uint32_t pb[2][2];
-                        split_f16(pd[0], pd[1], pb[0][0], pb[1][0]);
-                        split_f16(pd[2], pd[3], pb[0][1], pb[1][1]);
+                        uint32_t pb[SUB][2][2];
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) {
+                            float pd[4] = {pw[nb][u][0], pw[nb][u][1], pw[nb][u][2], pw[nb][u][3]};
+                            mul2(pd[0], pd[1], d[u][0], d[u][1]);
+                            mul2(pd[2], pd[3], d[u][2], d[u][3]);
+                            split_f16(pd[0], pd[1], pb[u][0][0], pb[u][1][0]);
+                            split_f16(pd[2], pd[3], pb[u][0][1], pb[u][1][1]);
+                        }
 #pragma unroll
                         for (int k2 = 0; k2 < 2; ++k2) {
                             float t[4];
-                            mma_16_0<false>(t, a[k2], pb[1][0], pb[1][1]);
-                            mma_16<false>(t, a[k2], pb[0][0], pb[0][1]);
+                            mma_16_0<false>(t, a[0][k2], pb[0][1][0], pb[0][1][1]);
+#pragma unroll
+                            for (int u = 1; u < SUB; ++u) mma_16<false>(t, a[u][k2], pb[u][1][0], pb[u][1][1]);
+#pragma unroll
+                            for (int u = 0; u < SUB; ++u) mma_16<false>(t, a[u][k2], pb[u][0][0], pb[u][0][1]);
                             fma2(acc[nb][2 * b + k2][0], acc[nb][2 * b + k2][1], t[0], t[1], back);
                             fma2(acc[nb][2 * b + k2][2], acc[nb][2 * b + k2][3], t[2], t[3], back);
                         }
                     }
                 }
             } else {
-                uint32_t pb[MB][NPP][2];
+                uint32_t pb[MB][SUB][NPP][2];
 #pragma unroll
                 for (int nb = 0; nb < MB; ++nb)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t w[3];
-                        if constexpr (TYPE == KV_F16) split_f16(sc[nb][2 * i], sc[nb][2 * i + 1], w[0], w[1]);
-                        else split_bf16(sc[nb][2 * i], sc[nb][2 * i + 1], w[0], w[1], w[2]);
+                    for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                        for (int k = 0; k < NPP; ++k) pb[nb][k][i] = movm_t(w[k]);
-                    }
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t w[3];
+                            if constexpr (TYPE == KV_F16) split_f16(sc[nb][u][2 * i], sc[nb][u][2 * i + 1], w[0], w[1]);
+                            else split_bf16(sc[nb][u][2 * i], sc[nb][u][2 * i + 1], w[0], w[1], w[2]);
+#pragma unroll
+                            for (int k = 0; k < NPP; ++k) pb[nb][u][k][i] = movm_t(w[k]);
+                        }
+                auto product = [&](float (&t)[4], const uint32_t (&r)[SUB][4], int nb) {     // the small parts first
+                    mma_16_0<PBF>(t, r[0], pb[nb][0][NPP - 1][0], pb[nb][0][NPP - 1][1]);
+#pragma unroll
+                    for (int k = NPP - 1; k >= 0; --k)
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u)
+                            if (k < NPP - 1 || u > 0) mma_16<PBF>(t, r[u], pb[nb][u][k][0], pb[nb][u][k][1]);
+                };
                 if (!mixed) {
 #pragma unroll
                     for (int i = 0; i < DP / 16; ++i) {
-                        uint32_t r[4];
-                        ldsm4t(r, va + G::at(v_row, 2 * i + v_chunk));
+                        uint32_t r[SUB][4];
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) ldsm4t(r[u], va + G::at(16 * u + v_row, 2 * i + v_chunk));
 #pragma unroll
                         for (int nb = 0; nb < MB; ++nb) {
                             float t[4];
-                            mma_16_0<PBF>(t, r, pb[nb][NPP - 1][0], pb[nb][NPP - 1][1]);
-#pragma unroll
-                            for (int k = NPP - 2; k >= 0; --k) mma_16<PBF>(t, r, pb[nb][k][0], pb[nb][k][1]);
+                            product(t, r, nb);
                             add2(acc[nb][i][0], acc[nb][i][1], t[0], t[1]);
                             add2(acc[nb][i][2], acc[nb][i][3], t[2], t[3]);
                         }
@@ -759,23 +893,26 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
                     const int tk1 = (min(row0 + G::ROWS, p.rows) - 1) / p.group;
                     for (int tk = row0 / p.group; tk <= tk1; ++tk) {
                         const int at = sq.first + tk;
-                        uint32_t z[2];                                    // of slots 2 c4, 2 c4 + 1 and + 8
+                        uint32_t z[SUB][2];                               // of slots 2 c4, 2 c4 + 1 and + 8
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int j = j0 + 8 * i + 2 * c4;
-                            z[i] = (attn_sees(p, at, j) ? 0xFFFFu : 0u) | (attn_sees(p, at, j + 1) ? 0xFFFF0000u : 0u);
-                        }
+                        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int j = j0 + 16 * u + 8 * i + 2 * c4;
+                                z[u][i] = (attn_sees(p, at, j) ? 0xFFFFu : 0u) | (attn_sees(p, at, j + 1) ? 0xFFFF0000u : 0u);
+                            }
 #pragma unroll
                         for (int i = 0; i < DP / 16; ++i) {
-                            uint32_t r[4];
-                            ldsm4t(r, va + G::at(v_row, 2 * i + v_chunk));
-                            r[0] &= z[0]; r[1] &= z[0]; r[2] &= z[1]; r[3] &= z[1];
+                            uint32_t r[SUB][4];
+#pragma unroll
+                            for (int u = 0; u < SUB; ++u) {
+                                ldsm4t(r[u], va + G::at(16 * u + v_row, 2 * i + v_chunk));
+                                r[u][0] &= z[u][0]; r[u][1] &= z[u][0]; r[u][2] &= z[u][1]; r[u][3] &= z[u][1];
+                            }
 #pragma unroll
                             for (int nb = 0; nb < MB; ++nb) {
                                 float t[4];
-                                mma_16_0<PBF>(t, r, pb[nb][NPP - 1][0], pb[nb][NPP - 1][1]);
-#pragma unroll
-                                for (int k = NPP - 2; k >= 0; --k) mma_16<PBF>(t, r, pb[nb][k][0], pb[nb][k][1]);
+                                product(t, r, nb);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
                                     if (s_at[nb * 8 + 2 * c4 + (e & 1)] == at) acc[nb][i][e] += t[e];
@@ -830,7 +967,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
             return p.out + (int64_t)(s * p.n_tok + t) * p.out_stride + (int64_t)(h * p.group + row0 + r - t * p.group) * p.dim;
         };
         auto put_stats = [&](int r, float mr, float lr) {
-            if (p.score) *reinterpret_cast<float2 *>(p.stats + 2 * ((int64_t)(s * p.n_kv + h) * p.rows + row0 + r)) = make_float2(mr, lr);
+            if (p.score) *reinterpret_cast<float2 *>(p.stats + 2 * ((int64_t)(s * p.n_kv + h) * p.raw_rows + row0 + r)) = make_float2(mr - p.l_shift, lr != 0.f ? __fdiv_rn(1.f, lr) : 0.f);
         };
         const bool whole = seg0 >= x0 && seg1 <= x1;
         const int slot = 2 * blockIdx.x + (seg0 >= x0 ? 1 : 0);
@@ -867,7 +1004,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
         }
         if (!whole) {
             // ---- the last CTA of the segment joins its parts, in CTA order
-            const int cta0 = (int)((unsigned)seg0 / share), cta1 = (int)((unsigned)(seg1 - 1) / share), n = cta1 - cta0 + 1;
+            const int cta0 = (int)((unsigned)seg0 / (unsigned)share), cta1 = (int)((unsigned)(seg1 - 1) / (unsigned)share), n = cta1 - cta0 + 1;
             __syncthreads();
             if (tid == 0) {
                 __threadfence();
@@ -877,7 +1014,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
             __syncthreads();
             if (s_last) {
                 if (tid == 0) p.counters[cta0] = 0u;
-                constexpr int CH = 8;                                     // parts in flight
+                constexpr int CH = 16;                                    // parts in flight
                 for (int i = tid; i < nrow * D4; i += NT) {
                     const int r = i / D4, d = i % D4;
                     if (4 * d >= p.dim) continue;
@@ -925,44 +1062,37 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
 
 // score[s][h][j] (+)= sum over the rows of 2^(s_j - m) / l, from the raw scores
 // and the joined (m, l) that attn_decode_kernel left in the workspace.  One
-// thread per slot, rows in order.
-constexpr int ATT_SCORE_THREADS = 256, ATT_SCORE_ROWS = 256;
+// thread per slot, rows in order.  It starts while that kernel ends, and what does
+// not come from it is read before the wait.
+constexpr int ATT_SCORE_THREADS = 256;
 
 static __global__ void __launch_bounds__(ATT_SCORE_THREADS) attn_score_kernel(const __grid_constant__ AttnParams p)
 {
-    __shared__ float2 s_st[ATT_SCORE_ROWS];                               // (m - l_shift, 1 / l; 0 for a row without weights)
     const int s = blockIdx.z, h = blockIdx.y;
     AttnSeq sq;
-    sq.set(attn_len(p, s), p);
+    sq.set<ATT_MIN_TILE>(attn_len(p, s), p);
     const int64_t sh = (int64_t)s * p.n_kv + h;
-    asm volatile("griddepcontrol.wait;" ::: "memory");                    // attn_decode_kernel is done
-    if ((int64_t)blockIdx.x * ATT_SCORE_THREADS >= sq.len) return;
-    for (int64_t b64 = (int64_t)blockIdx.x * ATT_SCORE_THREADS; b64 < sq.len; b64 += (int64_t)gridDim.x * ATT_SCORE_THREADS) {
-        const int j = (int)b64 + threadIdx.x;
-        const bool in = j < sq.len && sq.seen(j);
-        float v = 0.f;
-        for (int r0 = 0; r0 < p.rows; r0 += ATT_SCORE_ROWS) {
-            const int nr = min(ATT_SCORE_ROWS, p.rows - r0);
-            __syncthreads();
-            for (int r = threadIdx.x; r < nr; r += ATT_SCORE_THREADS) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.stats) + sh * p.rows + r0 + r);
-                s_st[r] = make_float2(ml.x - p.l_shift, ml.y != 0.f ? __fdiv_rn(1.f, ml.y) : 0.f);
-            }
-            __syncthreads();
-            if (in) {
-                const float *raw = p.raw + (sh * p.raw_stride + j) * p.raw_rows + r0;
-                for (int r = 0; r < nr; r += 2) {
-                    const float2 u = __ldcg(reinterpret_cast<const float2 *>(raw + r));
-                    if (s_st[r].y != 0.f) v += ex2(u.x - s_st[r].x) * s_st[r].y;
-                    if (r + 1 < nr && s_st[r + 1].y != 0.f) v += ex2(u.y - s_st[r + 1].x) * s_st[r + 1].y;
-                }
-            }
+    const float4 *st = reinterpret_cast<const float4 *>(p.stats + 2 * sh * p.raw_rows);      // of two rows
+    bool waited = false;
+    for (int64_t j64 = (int64_t)blockIdx.x * ATT_SCORE_THREADS + threadIdx.x; j64 < sq.len; j64 += (int64_t)gridDim.x * ATT_SCORE_THREADS) {
+        const int j = (int)j64;
+        if (!sq.seen(j)) continue;
+        float *o = p.score + sh * p.score_stride + j;
+        float v = j >= sq.first ? 0.f : *o;
+        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");       // attn_decode_kernel is done
+        waited = true;
+        const float2 *raw = reinterpret_cast<const float2 *>(p.raw + (sh * p.raw_stride + j) * p.raw_rows);
+        float given = 0.f;
+#pragma unroll 4
+        for (int r = 0; r < p.rows; r += 2) {
+            const float2 u = __ldcg(raw + r / 2);
+            const float4 w = __ldcg(st + r / 2);
+            given += w.y != 0.f ? ex2(u.x - w.x) * w.y : 0.f;
+            if (r + 1 < p.rows) given += w.w != 0.f ? ex2(u.y - w.z) * w.w : 0.f;
         }
-        if (in) {
-            float *o = p.score + sh * p.score_stride + j;
-            *o = j >= sq.first ? v : *o + v;
-        }
+        *o = v + given;
     }
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // One launch of the instance that holds p.dim and p.mb, on as many CTAs as run at
@@ -979,10 +1109,8 @@ static cudaError_t launch_attn_mb(const AttnParams &p, int sms, int64_t steps, c
 template <int TYPE>
 static cudaError_t launch_attn(const AttnParams &p, int sms, int64_t steps, cudaStream_t st)
 {
-    if (p.dim <= 64)
-        return p.mb == 1 ? launch_attn_mb<TYPE, 64, 1>(p, sms, steps, st) : p.mb == 2 ? launch_attn_mb<TYPE, 64, 2>(p, sms, steps, st) : launch_attn_mb<TYPE, 64, 4>(p, sms, steps, st);
-    if (p.dim <= 128)
-        return p.mb == 1 ? launch_attn_mb<TYPE, 128, 1>(p, sms, steps, st) : p.mb == 2 ? launch_attn_mb<TYPE, 128, 2>(p, sms, steps, st) : launch_attn_mb<TYPE, 128, 4>(p, sms, steps, st);
+    if (p.dim <= 64) return p.mb == 1 ? launch_attn_mb<TYPE, 64, 1>(p, sms, steps, st) : launch_attn_mb<TYPE, 64, 2>(p, sms, steps, st);
+    if (p.dim <= 128) return p.mb == 1 ? launch_attn_mb<TYPE, 128, 1>(p, sms, steps, st) : launch_attn_mb<TYPE, 128, 2>(p, sms, steps, st);
     return p.mb == 1 ? launch_attn_mb<TYPE, 256, 1>(p, sms, steps, st) : launch_attn_mb<TYPE, 256, 2>(p, sms, steps, st);
 }
 

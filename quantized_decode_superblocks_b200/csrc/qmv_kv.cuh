@@ -166,6 +166,7 @@ static __global__ void __launch_bounds__(EV_THREADS) kv_evict_kernel(const __gri
     __shared__ int s_sel[3];
     __shared__ int s_up[NW], s_eq[NW];
     const int h = blockIdx.x, s = blockIdx.y;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");              // the copy, which waits for this kernel's end
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int raw = __ldg(p.kv_len + s), n = min(max(raw, 0), p.max_len), m = min(n, p.budget);
     if (raw != n && tid == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);

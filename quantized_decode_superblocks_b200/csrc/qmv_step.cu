@@ -65,8 +65,6 @@ int page_shift(int page_size)
     return s;
 }
 
-// Row blocks of 8: as many as one CTA takes.
-int attn_mb(int rows, int dim) { return rows <= 8 ? 1 : rows <= 16 ? 2 : attn_max_mb(dim); }
 
 struct AttnWs {
     size_t ml, o, raw, stats, bytes;
@@ -82,17 +80,17 @@ int attn_ws(int type, int head_dim, int n_kv, int n_head, int n_seq, int n_tok, 
     if (n_head < 1 || n_head > MAX_HEADS || n_head % n_kv) return QMV_ERR_SHAPE;
     const int rows = n_head / n_kv * n_tok;
     if (rows > MAX_GROUP_ROWS) return QMV_ERR_SHAPE;
-    const int mb = attn_mb(rows, head_dim);
-    w.steps = ceil_div(rows, 8 * mb) * n_seq * n_kv * (slots / (ATT_TILE * ATT_NW) + 2);
+    const int mb = attn_mb(rows);
+    w.steps = ceil_div(rows, 8 * mb) * n_seq * n_kv * (slots / (ATT_MIN_TILE * ATT_NW) + 2);
     if (w.steps > INT_MAX) return QMV_ERR_SHAPE;
     const size_t parts = (size_t)2 * ATT_MAX_CTAS * 8 * mb;
-    w.raw_stride = ceil_div(slots, ATT_TILE) * ATT_TILE;
+    w.raw_stride = ceil_div(slots, ATT_MAX_TILE) * ATT_MAX_TILE;
     w.raw_rows = ceil_div(rows, 2) * 2;
     w.ml = up256(ATT_MAX_CTAS * sizeof(unsigned));
     w.o = w.ml + up256(parts * 2 * sizeof(float));
     w.raw = w.o + up256(parts * head_dim * sizeof(float));
-    const size_t all_rows = (size_t)n_seq * n_kv * rows;
-    w.stats = w.raw + (score ? up256((size_t)n_seq * n_kv * w.raw_rows * w.raw_stride * sizeof(float)) : 0);
+    const size_t all_rows = (size_t)n_seq * n_kv * w.raw_rows;
+    w.stats = w.raw + (score ? up256(all_rows * w.raw_stride * sizeof(float)) : 0);
     w.bytes = w.stats + (score ? up256(all_rows * 2 * sizeof(float)) : 0);
     return QMV_OK;
 }
@@ -162,7 +160,7 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     p.page_size = c.page_size;
     p.page_shift = page_shift(c.page_size);
     p.max_len = (int)(a->score ? std::min(slots, a->score_stride) : slots);
-    p.mb = attn_mb(p.rows, p.dim);
+    p.mb = attn_mb(p.rows);
     p.n_rb = (int)ceil_div(p.rows, 8 * p.mb);
     p.window = a->window >= slots ? 0 : a->window;      // every slot is within a window that long
     p.n_sink = a->n_sink;
