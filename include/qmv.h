@@ -375,11 +375,14 @@ int kv_append(const qmv_append *a, qmv_stream_t stream);
  *   softmax(s)_j,  f32, entry (s * n_kv_head + h) * score_stride + j;
  * the entries of the newest n_tok slots are set, not added to, so a new slot
  * needs no clearing; entries of slots that no query sees stay as they are.
- * q, out: f32, 16- and 4-byte aligned, token s * n_tok + t at + (s * n_tok + t) *
+ * q, out: f32, apart from each other, 16- and 4-byte aligned, token s * n_tok + t at + (s * n_tok + t) *
  * stride floats (q_stride a multiple of 4), heads one after another; n_head a
- * multiple of n_kv_head, 1 <= n_head / n_kv_head * n_tok <= 1024.
+ * multiple of n_kv_head, 1 <= n_head / n_kv_head * n_tok <= 1024.  The longest
+ * lengths, in steps of 64 slots, over all sequences and heads stay below 2^31.
  * Sums, maxima and products are f32; q and the weights reach the tensor cores
- * as exact sums of two f16 or three bf16 parts, so that no bits of f32 are lost.
+ * as sums of two f16 parts (f16 and Q8_0 caches: 22 bits, q's of the row's
+ * largest value) or three bf16 parts (24 bits).  Weighted sums are divided by
+ * the weights' sum at the end: values above 2^100 may overflow on the way.
  * The work of all sequences and heads is cut into equal shares, one per CTA;
  * sequences that several CTAs share are joined by the last one to finish, in a fixed
  * order: results do not vary from run to run.

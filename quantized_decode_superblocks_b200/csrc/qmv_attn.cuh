@@ -198,6 +198,14 @@ __device__ __forceinline__ void mma_16(float (&c)[4], const uint32_t (&a)[4], ui
     if constexpr (BF16) mma_bf16(c, a[0], a[1], a[2], a[3], b0, b1);
     else mma_f16(c, a[0], a[1], a[2], a[3], b0, b1);
 }
+// Adds 1 and returns the old value; what this CTA wrote before (and a barrier
+// ordered before this thread) is seen by who reads the sum, and the other way round.
+__device__ __forceinline__ unsigned atomic_inc_acq_rel(unsigned *p)
+{
+    unsigned old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+    return old;
+}
 // An 8x8 matrix of 16-bit values, two of a row per lane, transposed.
 __device__ __forceinline__ uint32_t movm_t(uint32_t x)
 {
@@ -276,10 +284,13 @@ struct AttnGeom {
     static constexpr int SC_BYTES = TYPE == KV_Q8_0 ? TILE * SC_PITCH : 0;
     static constexpr int STAGE = 2 * (KV_BYTES + SC_BYTES);      // one warp's stage: k | v | k scales | v scales
     static constexpr int ROWS = 8 * MB;
-    // Stages: about 96 KB of ring a CTA, two CTAs a SM (one where a stage is 16
-    // KB); 64 KB and three CTAs for 8 narrow rows, which have the registers for it.
-    static constexpr bool NARROW = MB == 1 && DP <= 64;
-    static constexpr int NST = NARROW ? (TYPE == KV_Q8_0 ? 4 : 2) : STAGE >= 8 * 1024 ? 3 : 5;
+    // Stages and CTAs a SM: three CTAs with up to 70 KB of shared memory where the
+    // registers allow it (8 narrow rows) or the arithmetic of Q8_0 needs the warps,
+    // else two with about 96 KB of ring, one where a stage is 16 KB.  Three against
+    // two: f16, 64 wide, one token over 131071 slots 53.5 -> 51.4 us; Q8_0, 128 wide,
+    // 8 tokens 43.0 -> 41.0 us; f16, 128 wide, 16 rows (two stages left) 46 -> 66 us.
+    static constexpr bool THREE = (MB == 1 && DP <= 64) || (TYPE == KV_Q8_0 && DP == 128);
+    static constexpr int NST = THREE ? (STAGE >= 8 * 1024 ? 2 : DP == 128 ? 3 : 4) : STAGE >= 8 * 1024 ? 3 : 5;
     static constexpr int RING = ATT_NW * NST * STAGE;
     static constexpr int NPQ = TYPE == KV_BF16 ? 3 : 2;          // parts of q
     static constexpr int NPP = TYPE == KV_BF16 ? 3 : 2;          // parts of the weights
@@ -289,8 +300,8 @@ struct AttnGeom {
     static constexpr int OPITCH = DP + 4;                        // floats: a store's rows in different banks
     static_assert(ATT_NW * ROWS * OPITCH * 4 <= RING, "the warps' outputs are joined in the ring");
     static constexpr int SMEM = RING + Q_BYTES;
-    static constexpr int CTAS = NARROW ? 3 : SMEM <= 110 * 1024 ? 2 : 1;          // on a SM
-    static_assert(!NARROW || SMEM <= 70 * 1024, "three CTAs' shared memory");
+    static constexpr int CTAS = THREE ? 3 : SMEM <= 110 * 1024 ? 2 : 1;           // on a SM
+    static_assert(!THREE || SMEM <= 70 * 1024, "three CTAs' shared memory");
     static_assert(SMEM <= 222 * 1024, "one CTA's shared memory");
     // 16-byte chunk c of slot r, so that 8 slots' chunks fall in different banks
     static __device__ __forceinline__ int mix(int r) { return NCHUNK >= 8 ? (r & 7) : ((r >> 1) & 3); }
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
     const int g = lane >> 2, c4 = lane & 3;
     const uint32_t ring0 = smem_addr(smem);
     const int units = p.n_rb * p.n_kv;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // attn_score_kernel, if it follows, waits for this one's end
+    if (p.score) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");          // attn_score_kernel, which waits for this one's end
 
     // ---- where this CTA's steps lie.  Every CTA gets `share` steps; where a little
     // more than the equal share lets each CTA stay within one segment (sequence, row
@@ -350,40 +361,66 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
         __syncthreads();
         return (unsigned)run * (unsigned)units;                           // below 2^31
     };
-    unsigned total = prefix([&](int s) {
-        const int raw = __ldg(p.kv_len + s);
-        if ((raw < 0 || raw > p.max_len) && blockIdx.x == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
-        return steps_of(s);
-    });
-    int share = (int)((total + gridDim.x - 1) / gridDim.x);
+    unsigned total;
+    int share;
     bool padded = false;
-    if (share > 1 && p.n_seq * units <= (int)gridDim.x) {
-        int4 n = make_int4(0, 0, 0, 0);                                   // CTAs at shares of share .. share + 3
-        for (int s = tid; s < p.n_seq; s += NT) {
-            const unsigned k = (unsigned)steps_of(s) - 1u;
-            n.x += k / (unsigned)share + 1u;
-            n.y += k / (unsigned)(share + 1) + 1u;
-            n.z += k / (unsigned)(share + 2) + 1u;
-            n.w += k / (unsigned)(share + 3) + 1u;
-        }
-        n.x = __reduce_add_sync(0xFFFFFFFFu, n.x);
-        n.y = __reduce_add_sync(0xFFFFFFFFu, n.y);
-        n.z = __reduce_add_sync(0xFFFFFFFFu, n.z);
-        n.w = __reduce_add_sync(0xFFFFFFFFu, n.w);
-        if (lane == 0) s_warp[warp] = n;
-        __syncthreads();
-        n = make_int4(0, 0, 0, 0);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            n.x += s_warp[w].x; n.y += s_warp[w].y; n.z += s_warp[w].z; n.w += s_warp[w].w;
-        }
-        __syncthreads();
+    auto choose = [&](int4 n) {                                           // n: CTAs at shares of share .. share + 3
         const int most = (int)gridDim.x, more = n.x * units <= most ? 0 : n.y * units <= most ? 1 : n.z * units <= most ? 2 : n.w * units <= most ? 3 : 4;
         padded = more < 4 && more <= share / 8 + 1;
         if (padded) share += more;
-    }
+    };
+    auto ctas_of = [&](int n) {
+        const unsigned k = (unsigned)n - 1u, d = (unsigned)share;
+        return n == 0 ? make_int4(0, 0, 0, 0) : make_int4(k / d + 1u, k / (d + 1u) + 1u, k / (d + 2u) + 1u, k / (d + 3u) + 1u);
+    };
+    auto reduce = [&](int4 n) {
+        return make_int4(__reduce_add_sync(0xFFFFFFFFu, n.x), __reduce_add_sync(0xFFFFFFFFu, n.y), __reduce_add_sync(0xFFFFFFFFu, n.z), __reduce_add_sync(0xFFFFFFFFu, n.w));
+    };
     auto length_of = [&](int n) { return padded ? (int)((unsigned)(n + share - 1) / (unsigned)share) * share : n; };
-    if (padded) total = prefix([&](int s) { return length_of(steps_of(s)); });
+    const bool few = p.n_seq <= 32;                                       // sequences: one a lane, every warp by itself
+    int my_len = 0, my_length = 0, my_pref = 0;
+    if (few) {
+        const int raw = lane < p.n_seq ? __ldg(p.kv_len + lane) : 0;
+        if ((raw < 0 || raw > p.max_len) && blockIdx.x == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
+        my_len = min(max(raw, 0), p.max_len);
+        AttnSeq q;
+        q.set<TILE>(my_len, p);
+        const int n = lane < p.n_seq ? q.n_steps : 0;
+        total = (unsigned)__reduce_add_sync(0xFFFFFFFFu, n) * (unsigned)units;
+        share = (int)((total + gridDim.x - 1) / gridDim.x);
+        if (share > 1 && p.n_seq * units <= (int)gridDim.x) choose(reduce(ctas_of(n)));
+        my_length = length_of(n);
+        int x = my_length;
+        for (int o = 1; o < p.n_seq; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        my_pref = x - my_length;
+        total = (unsigned)__shfl_sync(0xFFFFFFFFu, x, p.n_seq - 1) * (unsigned)units;
+    } else {
+        total = prefix([&](int s) {
+            const int raw = __ldg(p.kv_len + s);
+            if ((raw < 0 || raw > p.max_len) && blockIdx.x == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
+            return steps_of(s);
+        });
+        share = (int)((total + gridDim.x - 1) / gridDim.x);
+        if (share > 1 && p.n_seq * units <= (int)gridDim.x) {
+            int4 n = make_int4(0, 0, 0, 0);
+            for (int s = tid; s < p.n_seq; s += NT) {
+                const int4 c = ctas_of(steps_of(s));
+                n = make_int4(n.x + c.x, n.y + c.y, n.z + c.z, n.w + c.w);
+            }
+            n = reduce(n);
+            if (lane == 0) s_warp[warp] = n;
+            __syncthreads();
+            n = make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) n = make_int4(n.x + s_warp[w].x, n.y + s_warp[w].y, n.z + s_warp[w].z, n.w + s_warp[w].w);
+            __syncthreads();
+            choose(n);
+        }
+        if (padded) total = prefix([&](int s) { return length_of(steps_of(s)); });
+    }
     const int x0 = (int)min(total, (unsigned)share * blockIdx.x), x1 = (int)min(total, (unsigned)x0 + share);
 
     const int nchunk = p.dim * G::EB / 16;
@@ -398,19 +435,26 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
 
     for (int x = x0; x < x1;) {
         // ---- the segment: sequence, row block, head, and its steps in this CTA
-        int s = 0;
-        {
+        int s = 0, len, length, seq0;
+        if (few) {
+            s = __popc(__ballot_sync(0xFFFFFFFFu, lane < p.n_seq && my_pref * units <= x)) - 1;
+            len = __shfl_sync(0xFFFFFFFFu, my_len, s);
+            length = __shfl_sync(0xFFFFFFFFu, my_length, s);
+            seq0 = __shfl_sync(0xFFFFFFFFu, my_pref, s) * units;
+        } else {
             int hi = p.n_seq;
             while (hi - s > 1) {
                 const int mid = (s + hi) >> 1;
                 if (s_pref[mid] * units <= x) s = mid;
                 else hi = mid;
             }
+            len = attn_len(p, s);
+            length = length_of(steps_of(s));
+            seq0 = s_pref[s] * units;
         }
         AttnSeq sq;
-        sq.set<TILE>(attn_len(p, s), p);
-        const int seq0 = s_pref[s] * units;
-        const int length = length_of(sq.n_steps), unit = (int)((unsigned)(x - seq0) / (unsigned)length);
+        sq.set<TILE>(len, p);
+        const int unit = (int)((unsigned)(x - seq0) / (unsigned)length);
         const int h = p.n_rb == 1 ? unit : unit / p.n_rb, rb = unit - h * p.n_rb;        // a head's row blocks follow each other: the cache is in L2
         const int seg0 = seq0 + unit * length, seg1 = seg0 + length;
         const int row0 = rb * G::ROWS;
@@ -420,8 +464,11 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
         const int32_t *tab = p.table + (int64_t)s * p.table_stride;
         x = min(seg1, x1);
 
-        // ---- 8 narrow rows' q before the copies, behind which its loads would wait
-        float qraw[G::QREG ? DP / 16 : 1][4];
+        // ---- the warp's q rows (all warps' are the same 8, or those of block `warp`)
+        // before the copies, behind which their loads would wait
+        constexpr bool Q_EARLY = DP <= 128;
+        const int q_nb = G::QREG ? 0 : warp;
+        float qraw[Q_EARLY ? DP / 16 : 1][4];
         auto q_row = [&](int row) {
             const int tok = row < p.rows ? row / p.group : 0;
             return p.q + (int64_t)(s * p.n_tok + tok) * p.q_stride + (int64_t)(h * p.group + (row < p.rows ? row - tok * p.group : 0)) * p.dim;
@@ -433,10 +480,12 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
             const float2 b = ok ? __ldg(reinterpret_cast<const float2 *>(x + d1)) : make_float2(0.f, 0.f);
             f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
         };
-        if constexpr (G::QREG) {
-            const float *x = q_row(row0 + g);
+        if constexpr (Q_EARLY) {
+            const int row = row0 + q_nb * 8 + g;
+            const bool ok = q_nb < MB && row < p.rows;
+            const float *x = q_row(ok ? row : 0);
 #pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks) q_load4(x, row0 + g < p.rows, ks, qraw[ks]);
+            for (int ks = 0; ks < DP / 16; ++ks) q_load4(x, ok, ks, qraw[ks]);
         }
 
         // ---- the ring: page entries one step ahead of the copies
@@ -529,7 +578,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
             const int row = row0 + nb * 8 + g;
             const float *x = q_row(row);
             auto load4 = [&](int ks, float (&f)[4]) {
-                if constexpr (G::QREG) {
+                if constexpr (Q_EARLY) {
                     f[0] = qraw[ks][0]; f[1] = qraw[ks][1]; f[2] = qraw[ks][2]; f[3] = qraw[ks][3];
                 } else {
                     q_load4(x, row < p.rows, ks, f);
@@ -1006,33 +1055,28 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
             // ---- the last CTA of the segment joins its parts, in CTA order
             const int cta0 = (int)((unsigned)seg0 / (unsigned)share), cta1 = (int)((unsigned)(seg1 - 1) / (unsigned)share), n = cta1 - cta0 + 1;
             __syncthreads();
-            if (tid == 0) {
-                __threadfence();
-                s_last = atomicAdd(p.counters + cta0, 1u) == (unsigned)(n - 1);
-                __threadfence();
-            }
+            if (tid == 0) s_last = atomic_inc_acq_rel(p.counters + cta0) == (unsigned)(n - 1);
             __syncthreads();
             if (s_last) {
                 if (tid == 0) p.counters[cta0] = 0u;
                 constexpr int CH = 16;                                    // parts in flight
-                for (int i = tid; i < nrow * D4; i += NT) {
-                    const int r = i / D4, d = i % D4;
-                    if (4 * d >= p.dim) continue;
-                    // part c: the second of CTA cta0's two slots for c = 0, else the first of CTA cta0 + c's
+                // part c: the second of CTA cta0's two slots for c = 0, else the first of CTA cta0 + c's
+                const int64_t po_step = (int64_t)G::ROWS * p.dim;
+                auto join = [&](int r, int d, int c_first, int c_step, float4 &v, float &mr, float &lr) {
                     const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + (int64_t)2 * cta0 * G::ROWS + r;
                     const float *po = p.part_o + ((int64_t)2 * cta0 * G::ROWS + r) * p.dim + 4 * d;
-                    const int64_t po_step = (int64_t)G::ROWS * p.dim;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float mr = -INFINITY, lr = 0.f;
-                    for (int c0 = 0; c0 < n; c0 += CH) {
+                    v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    mr = -INFINITY;
+                    lr = 0.f;
+                    for (int c0 = c_first; c0 < n; c0 += CH * c_step) {
                         float2 q[CH];
                         float4 u[CH];
 #pragma unroll
                         for (int k = 0; k < CH; ++k) {
-                            const int sl = c0 + k == 0 ? 1 : 2 * (c0 + k);
+                            const int c = c0 + k * c_step, sl = c == 0 ? 1 : 2 * c;
                             q[k] = make_float2(-INFINITY, 0.f);
                             u[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (c0 + k < n) {
+                            if (c < n) {
                                 q[k] = __ldcg(ml + sl * G::ROWS);
                                 u[k] = __ldcg(reinterpret_cast<const float4 *>(po + sl * po_step));
                             }
@@ -1051,8 +1095,38 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
                             v.x += f * u[k].x; v.y += f * u[k].y; v.z += f * u[k].z; v.w += f * u[k].w;
                         }
                     }
-                    put(r, d, v, lr);
-                    if (d == 0) put_stats(r, mr, lr);
+                };
+                float4 v;
+                float mr, lr;
+                if (nrow * D4 <= NT / 2 && n > CH) {                      // many parts of few rows: two threads take every other one
+                    float4 *sv = reinterpret_cast<float4 *>(smem);
+                    float2 *sm = reinterpret_cast<float2 *>(smem + NT / 2 * sizeof(float4));
+                    const int half = tid / (NT / 2), i = tid % (NT / 2), r = i / D4, d = i % D4;
+                    const bool in = i < nrow * D4 && 4 * d < p.dim;
+                    if (in) {
+                        join(r, d, half, 2, v, mr, lr);
+                        if (half) {
+                            sv[i] = v;
+                            sm[i] = make_float2(mr, lr);
+                        }
+                    }
+                    __syncthreads();
+                    if (in && !half) {
+                        const float4 w = sv[i];
+                        const float2 q = sm[i];
+                        const float mn = fmaxf(mr, q.x), f = mr == mn ? 1.f : ex2(mr - mn), g2 = q.x == mn ? 1.f : ex2(q.x - mn);
+                        lr = f * lr + g2 * q.y;
+                        put(r, d, make_float4(f * v.x + g2 * w.x, f * v.y + g2 * w.y, f * v.z + g2 * w.z, f * v.w + g2 * w.w), lr);
+                        if (d == 0) put_stats(r, mn, lr);
+                    }
+                } else {
+                    for (int i = tid; i < nrow * D4; i += NT) {
+                        const int r = i / D4, d = i % D4;
+                        if (4 * d >= p.dim) continue;
+                        join(r, d, 0, 1, v, mr, lr);
+                        put(r, d, v, lr);
+                        if (d == 0) put_stats(r, mr, lr);
+                    }
                 }
             }
         }

@@ -95,6 +95,13 @@ int attn_ws(int type, int head_dim, int n_kv, int n_head, int n_seq, int n_tok, 
     return QMV_OK;
 }
 
+// Whether an output of `bytes` bytes at `out` shares memory with an input.
+bool overlap(const void *out, int64_t out_bytes, const void *in, int64_t in_bytes)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(in);
+    return a < b ? b - a < (uintptr_t)out_bytes : a - b < (uintptr_t)in_bytes;
+}
+
 int finish(cudaError_t e) { return e == cudaSuccess ? QMV_OK : host_cuda_fail(e); }
 
 }  // namespace
@@ -128,6 +135,7 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     if (a->window < 0 || a->n_sink < 0 || !(a->scale - a->scale == 0.f)) return QMV_ERR_SHAPE;
     if (!aligned(a->q, 16) || a->q_stride % 4 || !aligned(a->out, 4) || !aligned(a->score, 4) || !aligned(a->block_table, 4) ||
         !aligned(a->kv_len, 4) || !aligned(a->workspace, 256)) return QMV_ERR_ALIGN;
+    if (a->out == a->q) return QMV_ERR_SHAPE;
     if (a->workspace_bytes < w.bytes) return QMV_ERR_WS;
     if (host_injected_failure()) return QMV_ERR_CUDA;
     HostDev di;
@@ -202,6 +210,7 @@ int kv_append(const qmv_append *a, qmv_stream_t stream)
     if (a->rope_style != QMV_ROPE_HALVES && a->rope_style != QMV_ROPE_PAIRS) return QMV_ERR_SHAPE;
     const int64_t width = (int64_t)c.n_kv_head * c.head_dim, q_width = (int64_t)a->n_head * c.head_dim;
     if (!stride_ok(a->k_stride, width) || !stride_ok(a->v_stride, width)) return QMV_ERR_SHAPE;
+    if (a->q && a->q == a->q_out && a->q_stride != a->q_out_stride) return QMV_ERR_SHAPE;
     if (a->q && (a->n_head < 1 || a->n_head > MAX_HEADS || !stride_ok(a->q_stride, q_width) || !stride_ok(a->q_out_stride, q_width))) return QMV_ERR_SHAPE;
     for (const void *x : {(const void *)a->q, (const void *)a->k, (const void *)a->v, (const void *)a->q_out, (const void *)a->block_table,
                           (const void *)a->kv_len, (const void *)a->pos, (const void *)a->inv_freq})
@@ -265,6 +274,9 @@ int kv_evict(const qmv_evict *a, qmv_stream_t stream)
     for (const void *x : {(const void *)a->score, (const void *)a->score_out, (const void *)a->block_table, (const void *)a->kv_len,
                           (const void *)a->dst_table, (const void *)a->kept, (const void *)a->len_out})
         if (!aligned(x, 4)) return QMV_ERR_ALIGN;
+    const int64_t rows = (int64_t)a->n_seq * c.n_kv_head;
+    if (overlap(a->score_out, ((rows - 1) * a->score_out_stride + a->budget) * 4, a->score, ((rows - 1) * a->score_stride + std::min(slots, a->score_stride)) * 4) ||
+        overlap(a->len_out, (int64_t)a->n_seq * 4, a->kv_len, (int64_t)a->n_seq * 4)) return QMV_ERR_SHAPE;
     if (host_injected_failure()) return QMV_ERR_CUDA;
     HostDev di;
     if ((rc = host_dev(di))) return rc;

@@ -41,20 +41,20 @@ def filled(cls, base, kw, c):
 
 
 def attn(L, c=None, **kw):
-    base = dict(q=A, out=A, score=None, q_stride=2048, out_stride=2048, score_stride=0, n_head=32, n_seq=2, n_tok=1, max_pages=4,
+    base = dict(q=A, out=2 * A, score=None, q_stride=2048, out_stride=2048, score_stride=0, n_head=32, n_seq=2, n_tok=1, max_pages=4,
                 table_stride=4, block_table=A, kv_len=A, scale=0.125, window=0, n_sink=0, workspace=A, workspace_bytes=1 << 40)
     return L.attn_decode(ctypes.byref(filled(q.AttnArgs, base, kw, c)), None)
 
 
 def append(L, c=None, **kw):
-    base = dict(q=A, k_in=A, v_in=A, q_out=A, q_stride=3000, k_stride=3000, v_stride=3000, q_out_stride=2048, n_head=32, n_seq=2,
+    base = dict(q=A, k_in=A, v_in=A, q_out=2 * A, q_stride=3000, k_stride=3000, v_stride=3000, q_out_stride=2048, n_head=32, n_seq=2,
                 n_tok=1, rope_dim=64, rope_style=0, max_pages=4, table_stride=4, block_table=A, kv_len=A, pos=None, inv_freq=A)
     return L.kv_append(ctypes.byref(filled(q.AppendArgs, base, kw, c)), None)
 
 
 def evict(L, c=None, **kw):
-    base = dict(score=A, score_out=A, score_stride=64, score_out_stride=32, n_seq=2, max_pages=4, dst_max_pages=2, keep_first=4,
-                keep_last=8, budget=32, table_stride=4, dst_table_stride=2, block_table=A, kv_len=A, dst_table=A, kept=A, len_out=A)
+    base = dict(score=A, score_out=2 * A, score_stride=64, score_out_stride=32, n_seq=2, max_pages=4, dst_max_pages=2, keep_first=4,
+                keep_last=8, budget=32, table_stride=4, dst_table_stride=2, block_table=A, kv_len=A, dst_table=A, kept=A, len_out=3 * A)
     return L.kv_evict(ctypes.byref(filled(q.EvictArgs, base, kw, c)), None)
 
 
@@ -129,6 +129,17 @@ def test_attn_checks(L):
     assert q.attn_ws_bytes(cache(type=7), 32, 2, 1, 4) == 0
     assert L.attn_decode(None, None) == NULL
     assert "workspace" in q.strerror(WS)
+    assert attn(L, out=A) == SHAPE                      # other CTAs may still read the queries
+
+
+def test_outputs_that_share_memory_with_inputs_are_refused(L):
+    assert append(L, q_out=A, q_stride=3000, q_out_stride=2048) == SHAPE and good(L, append, q_out=A, q_stride=2048, q_out_stride=2048)
+    rows = 2 * 8                                        # scores of 64 floats a row, the last one whole
+    assert evict(L, score_out=A) == SHAPE and evict(L, score_out=A + rows * 64 * 4 - 4) == SHAPE
+    assert good(L, evict, score_out=A + rows * 64 * 4)
+    assert evict(L, score=2 * A + rows * 32 * 4 - 4) == SHAPE and good(L, evict, score=2 * A + rows * 32 * 4)
+    assert evict(L, len_out=A) == SHAPE and evict(L, len_out=A + 4) == SHAPE and good(L, evict, len_out=A + 8)
+    assert evict(L, kv_len=3 * A + 4) == SHAPE and good(L, evict, kv_len=3 * A + 8)
 
 
 def test_append_checks(L):
