@@ -1135,10 +1135,10 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
 }
 
 // score[s][h][j] (+)= sum over the rows of 2^(s_j - m) / l, from the raw scores
-// and the joined (m, l) that attn_decode_kernel left in the workspace.  One
-// thread per slot, rows in order.  It starts while that kernel ends, and what does
+// and the joined (m, l) that attn_decode_kernel left in the workspace.  Two
+// slots a thread, rows in order.  It starts while that kernel ends, and what does
 // not come from it is read before the wait.
-constexpr int ATT_SCORE_THREADS = 256;
+constexpr int ATT_SCORE_THREADS = 256, ATT_SCORE_SLOTS = 2 * ATT_SCORE_THREADS;
 
 static __global__ void __launch_bounds__(ATT_SCORE_THREADS) attn_score_kernel(const __grid_constant__ AttnParams p)
 {
@@ -1148,23 +1148,31 @@ static __global__ void __launch_bounds__(ATT_SCORE_THREADS) attn_score_kernel(co
     const int64_t sh = (int64_t)s * p.n_kv + h;
     const float4 *st = reinterpret_cast<const float4 *>(p.stats + 2 * sh * p.raw_rows);      // of two rows
     bool waited = false;
-    for (int64_t j64 = (int64_t)blockIdx.x * ATT_SCORE_THREADS + threadIdx.x; j64 < sq.len; j64 += (int64_t)gridDim.x * ATT_SCORE_THREADS) {
-        const int j = (int)j64;
-        if (!sq.seen(j)) continue;
-        float *o = p.score + sh * p.score_stride + j;
-        float v = j >= sq.first ? 0.f : *o;
-        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");       // attn_decode_kernel is done
+    for (int64_t base = (int64_t)blockIdx.x * ATT_SCORE_SLOTS; base < sq.len; base += (int64_t)gridDim.x * ATT_SCORE_SLOTS) {
+        int j[2];
+        bool in[2];
+        float v[2], given[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            j[k] = (int)min(base + k * ATT_SCORE_THREADS + threadIdx.x, (int64_t)sq.len);
+            in[k] = sq.seen(j[k]);
+            v[k] = in[k] && j[k] < sq.first ? p.score[sh * p.score_stride + j[k]] : 0.f;
+        }
+        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");   // attn_decode_kernel is done
         waited = true;
-        const float2 *raw = reinterpret_cast<const float2 *>(p.raw + (sh * p.raw_stride + j) * p.raw_rows);
-        float given = 0.f;
 #pragma unroll 4
         for (int r = 0; r < p.rows; r += 2) {
-            const float2 u = __ldcg(raw + r / 2);
             const float4 w = __ldcg(st + r / 2);
-            given += w.y != 0.f ? ex2(u.x - w.x) * w.y : 0.f;
-            if (r + 1 < p.rows) given += w.w != 0.f ? ex2(u.y - w.z) * w.w : 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 u = in[k] ? __ldcg(reinterpret_cast<const float2 *>(p.raw + (sh * p.raw_stride + j[k]) * p.raw_rows + r)) : make_float2(0.f, 0.f);
+                given[k] += w.y != 0.f ? ex2(u.x - w.x) * w.y : 0.f;
+                if (r + 1 < p.rows) given[k] += w.w != 0.f ? ex2(u.y - w.z) * w.w : 0.f;
+            }
         }
-        *o = v + given;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (in[k]) p.score[sh * p.score_stride + j[k]] = v[k] + given[k];
     }
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
