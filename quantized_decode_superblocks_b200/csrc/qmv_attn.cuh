@@ -856,9 +856,18 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             d[u][i] = half_bits_to_float(lds_u16(sa + (16 * u + 2 * c4 + (i & 1) + (i >> 1) * 8) * G::SC_PITCH));
-                            if (mixed && !(fabsf(d[u][i]) < INFINITY)) d[u][i] = 0.f;       // NaN of a slot that this row may not see: its weight is 0
                             dm = fmaxf(dm, fabsf(d[u][i]));
                         }
+                    if (mixed) {                                          // NaN or infinity of a slot that a row may not see: its weight is 0
+                        dm = 0.f;
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (!(fabsf(d[u][i]) < INFINITY)) d[u][i] = 0.f;
+                                dm = fmaxf(dm, fabsf(d[u][i]));
+                            }
+                    }
                     // the scales over a power of two at least the largest of them: their products with the weights stay in f16
                     dm = fmaxf(dm, __shfl_xor_sync(0xFFFFFFFFu, dm, 1));
                     dm = fmaxf(dm, __shfl_xor_sync(0xFFFFFFFFu, dm, 2));

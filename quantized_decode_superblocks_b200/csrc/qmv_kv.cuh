@@ -126,15 +126,19 @@ static __global__ void __launch_bounds__(APP_THREADS, APP_CTAS) kv_append_kernel
 // how many slots with exactly that key are kept (the lowest ones).  A round that
 // leaves no slot undecided is the last one: scores that all differ need two.
 // Then each warp writes the kept slots of its part in order, at the place that
-// the counts of the warps before it give.  (Spread over a cluster of 8 CTAs,
-// the counts' way through distributed shared memory cost more than it saved:
-// 4352 slots 7.6 us, 16 x 8 x 16384 slots 10 us, against FIXME here.)
+// the counts of the warps before it give: one cache of 4352 slots 5 us, 16 of
+// up to 16384 slots 11 us, bound by the instructions of one SM per head.  (Spread over
+// a cluster of 8 CTAs, whose counts went through distributed shared memory:
+// 12 us, and 18 us in each of three waves.)
 //
-// Copy: a warp per 32 (rows over 256 bytes: 16) kept slots of a (sequence, head),
-// the heads of the same slots next to each other.
+// Copy: a warp per EV_SLOTS kept slots of a (sequence, head), the heads of the
+// same slots next to each other; 16 x 8 heads x 4096 slots of 512 bytes, in and
+// out, 87 us, 6.2 TB/s.  (With 32 slots a warp, k and v by the same lane: 95 us.  By
+// 16-byte loads and stores through registers 104 to 130 us, depending on how
+// many a lane has in flight.)
 constexpr int EV_THREADS = 1024, EV_BINS = 2048;
 constexpr int EV_KEYS = 40960;                // keys that shared memory holds; those of later slots are made anew in every round
-constexpr int EV_COPY_THREADS = 128;
+constexpr int EV_COPY_THREADS = 128, EV_SLOTS = 16;     // slots: of a warp of the copy
 
 struct EvictParams {
     uint8_t *k, *v, *ks, *vs;
@@ -146,7 +150,6 @@ struct EvictParams {
     int32_t *kept, *len_out;
     int32_t n_kv, page_size, max_len, keep_first, keep_last, budget;
     int32_t row_bytes, scale_words, eb;       // of one slot and head; scale_words: 4-byte words of its scales
-    int32_t copy_slots;                       // of a warp of the copy
     int *err;
 };
 
@@ -299,16 +302,16 @@ static __global__ void __launch_bounds__(EV_THREADS) kv_evict_kernel(const __gri
     if (h == 0 && tid == 0) p.len_out[s] = m;
 }
 
-// A lane per slot: its rows of k and v go through shared memory by bulk copies,
-// its scales (too short for one) through registers.
+// A lane per row of k or v, which goes through shared memory by bulk copies; its
+// scales (too short for one) go through registers.
 static __global__ void __launch_bounds__(EV_COPY_THREADS) kv_evict_copy_kernel(const __grid_constant__ EvictParams p)
 {
-    extern __shared__ __align__(128) uint8_t s_rows[];                            // [warps][slots][k | v]
+    extern __shared__ __align__(128) uint8_t s_rows[];                            // [warps][k, v][slots]
     __shared__ __align__(8) uint64_t s_bar[EV_COPY_THREADS / 32];
     const int h = blockIdx.x % p.n_kv, s = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int m = min(min(max(__ldg(p.kv_len + s), 0), p.max_len), p.budget);
-    const int i = (blockIdx.x / p.n_kv * (EV_COPY_THREADS / 32) + warp) * p.copy_slots + lane;
-    const bool in = lane < p.copy_slots && i < m;
+    const int i = (blockIdx.x / p.n_kv * (EV_COPY_THREADS / 32) + warp) * EV_SLOTS + lane % EV_SLOTS;
+    const bool in = lane < 2 * EV_SLOTS && i < m;
     const int pd = in ? __ldg(p.dst_table + (int64_t)s * p.dst_table_stride + i / p.page_size) : -1;
     const uint32_t bar = smem_addr(s_bar + warp);
     if (lane == 0) {
@@ -328,26 +331,21 @@ static __global__ void __launch_bounds__(EV_COPY_THREADS) kv_evict_copy_kernel(c
     }
     const uint32_t n_ok = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, ok)), rb = (uint32_t)p.row_bytes;
     if (n_ok == 0) return;
-    const uint32_t row = smem_addr(s_rows) + (uint32_t)(warp * p.copy_slots + lane) * 2 * rb;
-    if (lane == 0) mbar_arrive_expect_tx(bar, n_ok * 2 * rb);
+    const uint32_t row = smem_addr(s_rows) + (uint32_t)(warp * 2 * EV_SLOTS + lane) * rb;
+    uint8_t *pool = lane < EV_SLOTS ? p.k : p.v, *scales = lane < EV_SLOTS ? p.ks : p.vs;
+    if (lane == 0) mbar_arrive_expect_tx(bar, n_ok * rb);
     __syncwarp();
     if (ok) {
-        bulk_g2s(row, p.k + es * p.eb, rb, bar);
-        bulk_g2s(row + rb, p.v + es * p.eb, rb, bar);
-        for (int c = 0; c < p.scale_words; ++c) {
-            const uint32_t x = __ldg(reinterpret_cast<const uint32_t *>(p.ks + es / 16) + c);
-            const uint32_t y = __ldg(reinterpret_cast<const uint32_t *>(p.vs + es / 16) + c);
-            reinterpret_cast<uint32_t *>(p.ks + ed / 16)[c] = x;
-            reinterpret_cast<uint32_t *>(p.vs + ed / 16)[c] = y;
-        }
+        bulk_g2s(row, pool + es * p.eb, rb, bar);
+        for (int c = 0; c < p.scale_words; ++c)
+            reinterpret_cast<uint32_t *>(scales + ed / 16)[c] = __ldg(reinterpret_cast<const uint32_t *>(scales + es / 16) + c);
     }
     if (!mbar_wait_bounded(bar, 0)) {
         atomicOr(p.err, mbar_wait_bounded(bar, 0) ? 2 : 2 | 4 /* QMV_DEVERR_TIMEOUT, QMV_DEVERR_DRAIN */);
         return;
     }
     if (ok) {
-        bulk_s2g(p.k + ed * p.eb, row, rb);
-        bulk_s2g(p.v + ed * p.eb, row + rb, rb);
+        bulk_s2g(pool + ed * p.eb, row, rb);
         bulk_s2g_drain();
     }
 }

@@ -62,9 +62,9 @@ static __global__ void __launch_bounds__(LG_THREADS) logits_argmax_kernel(const 
     __shared__ uint2 s_best[LG_THREADS / 32];
     const int row = blockIdx.y, v0 = blockIdx.x * p.slice, nv = min(p.slice, p.vocab - v0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool pushed = p.hist || p.bias_ids;
     const int n_hist = p.hist ? (int)min((int64_t)max(0, __ldg(p.hist_len + row)), p.hist_stride) : 0;
     const int n_bias = p.bias_ids ? (int)min((int64_t)max(0, __ldg(p.bias_len + row)), p.bias_stride) : 0;
+    const bool pushed = n_hist > 0 || n_bias > 0;
     const float *logits = p.logits + (int64_t)row * p.logits_stride + v0;
     const uint32_t *mask = p.mask ? p.mask + (int64_t)row * p.mask_stride + (v0 >> 5) : nullptr;
     float *out = p.out ? p.out + (int64_t)row * p.out_stride + v0 : nullptr;

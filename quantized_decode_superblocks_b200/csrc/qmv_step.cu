@@ -310,7 +310,6 @@ int kv_evict(const qmv_evict *a, qmv_stream_t stream)
     p.eb = c.type == QMV_KV_Q8_0 ? 1 : 2;
     p.row_bytes = c.head_dim * p.eb;
     p.scale_words = c.type == QMV_KV_Q8_0 ? c.head_dim / 64 : 0;
-    p.copy_slots = p.row_bytes <= 256 ? 32 : 16;
     p.err = di.err;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     static SmemCfg configured_choice, configured;
@@ -318,7 +317,7 @@ int kv_evict(const qmv_evict *a, qmv_stream_t stream)
     const cudaError_t e = launch_with(kv_evict_kernel, configured_choice, p, dim3((unsigned)c.n_kv_head, (unsigned)a->n_seq), smem, st, false, false, EV_THREADS);
     if (e != cudaSuccess) return finish(e);
     // launched while the choice runs (it waits for its end itself)
-    const int per = EV_COPY_THREADS / 32 * p.copy_slots;
+    const int per = EV_COPY_THREADS / 32 * EV_SLOTS;
     const int64_t gx = ceil_div(std::min(p.budget, p.max_len), per) * c.n_kv_head;           // at most 2^31 / 64 * 1024 / 16: budget slots fit the table
     if (gx > INT_MAX) return QMV_ERR_SHAPE;
     return finish(launch_with(kv_evict_copy_kernel, configured, p, dim3((unsigned)gx, (unsigned)a->n_seq), (size_t)per * 2 * p.row_bytes, st, true, false, EV_COPY_THREADS));
