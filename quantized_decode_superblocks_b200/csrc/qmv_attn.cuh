@@ -53,8 +53,9 @@ namespace qmv {
 
 enum { KV_F16 = 0, KV_BF16 = 1, KV_Q8_0 = 2 };
 
-constexpr int ATT_NW = 4;                    // warps of a CTA
-constexpr int ATT_THREADS = ATT_NW * 32;
+// Warps of a CTA; 6 where a stage is 16 KB and one CTA fills the SM.
+__host__ __device__ constexpr int attn_warps(int type, int dp) { return dp > 128 && type != 2 ? 6 : 4; }
+constexpr int ATT_MIN_NW = 4;
 // Slots of a tile: 32 where its keys and values are short and registers allow, so
 // that a warp's work around a tile is spread over more of them.  Against 16: f16,
 // 64 wide, one token over 131071 slots 60 -> 54 us; Q8_0, 128 wide, one token for
@@ -104,7 +105,7 @@ struct AttnSeq {
     int sink_tiles, base;  // tiles 0 .. sink_tiles - 1 start at slot 0, the others at slot base
     int n_tiles, n_steps;  // at least 1, so that every row gets written
 
-    template <int TILE>
+    template <int TILE, int NW>
     __device__ __forceinline__ void set(int n, const AttnParams &p)
     {
         len = n;
@@ -118,7 +119,7 @@ struct AttnSeq {
             if (sinks > 0 && sink_tiles * TILE >= base) sink_tiles = base = 0;   // the parts meet
         }
         n_tiles = max(1, sink_tiles + (len - base + TILE - 1) / TILE);
-        n_steps = (n_tiles + ATT_NW - 1) / ATT_NW;
+        n_steps = (n_tiles + NW - 1) / NW;
     }
     template <int TILE>
     __device__ __forceinline__ int slot0(int tile) const
@@ -284,21 +285,22 @@ struct AttnGeom {
     static constexpr int SC_BYTES = TYPE == KV_Q8_0 ? TILE * SC_PITCH : 0;
     static constexpr int STAGE = 2 * (KV_BYTES + SC_BYTES);      // one warp's stage: k | v | k scales | v scales
     static constexpr int ROWS = 8 * MB;
+    static constexpr int NW = attn_warps(TYPE, DP), THREADS = NW * 32;
     // Stages and CTAs a SM: three CTAs with up to 70 KB of shared memory where the
     // registers allow it (8 narrow rows) or the arithmetic of Q8_0 needs the warps,
     // else two with about 96 KB of ring, one where a stage is 16 KB.  Three against
     // two: f16, 64 wide, one token over 131071 slots 53.5 -> 51.4 us; Q8_0, 128 wide,
     // 8 tokens 43.0 -> 41.0 us; f16, 128 wide, 16 rows (two stages left) 46 -> 66 us.
     static constexpr bool THREE = (MB == 1 && DP <= 64) || (TYPE == KV_Q8_0 && DP == 128);
-    static constexpr int NST = THREE ? (STAGE >= 8 * 1024 ? 2 : DP == 128 ? 3 : 4) : STAGE >= 8 * 1024 ? 3 : 5;
-    static constexpr int RING = ATT_NW * NST * STAGE;
+    static constexpr int NST = DP > 128 ? 2 : THREE ? (STAGE >= 8 * 1024 ? 2 : DP == 128 ? 3 : 4) : STAGE >= 8 * 1024 ? 3 : 5;
+    static constexpr int RING = NW * NST * STAGE;
     static constexpr int NPQ = TYPE == KV_BF16 ? 3 : 2;          // parts of q
     static constexpr int NPP = TYPE == KV_BF16 ? 3 : 2;          // parts of the weights
     static constexpr bool QREG = MB == 1 && DP <= 128;           // q's operand fragments in registers
     static constexpr int QW = 2 * NPQ;                           // words of q per lane and 16 columns
     static constexpr int Q_BYTES = QREG ? 0 : MB * (DP / 16) * 32 * QW * 4;
     static constexpr int OPITCH = DP + 4;                        // floats: a store's rows in different banks
-    static_assert(ATT_NW * ROWS * OPITCH * 4 <= RING, "the warps' outputs are joined in the ring");
+    static_assert(NW * ROWS * OPITCH * 4 <= RING, "the warps' outputs are joined in the ring");
     static constexpr int SMEM = RING + Q_BYTES;
     static constexpr int CTAS = THREE ? 3 : SMEM <= 110 * 1024 ? 2 : 1;           // on a SM
     static_assert(!THREE || SMEM <= 70 * 1024, "three CTAs' shared memory");
@@ -309,10 +311,10 @@ struct AttnGeom {
 };
 
 template <int TYPE, int DP, int MB>
-__global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) attn_decode_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE, DP, MB>::CTAS) attn_decode_kernel(const __grid_constant__ AttnParams p)
 {
     using G = AttnGeom<TYPE, DP, MB>;
-    constexpr int NW = ATT_NW, NT = ATT_THREADS, NPQ = G::NPQ, NPP = G::NPP, QW = G::QW, TILE = G::TILE, SUB = G::SUB;
+    constexpr int NW = G::NW, NT = G::THREADS, NPQ = G::NPQ, NPP = G::NPP, QW = G::QW, TILE = G::TILE, SUB = G::SUB;
     constexpr bool PBF = TYPE == KV_BF16;                        // type of the second product's parts
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_pref[ATT_MAX_SEQ + 1];                      // steps of one head before each sequence
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
     // its ring nor joins twice.
     auto steps_of = [&](int s) {
         AttnSeq q;
-        q.set<TILE>(attn_len(p, s), p);
+        q.set<TILE, NW>(attn_len(p, s), p);
         return q.n_steps;
     };
     auto prefix = [&](auto &&length) {                                    // s_pref[s] = sum of the lengths before sequence s
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
         if ((raw < 0 || raw > p.max_len) && blockIdx.x == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
         my_len = min(max(raw, 0), p.max_len);
         AttnSeq q;
-        q.set<TILE>(my_len, p);
+        q.set<TILE, NW>(my_len, p);
         const int n = lane < p.n_seq ? q.n_steps : 0;
         total = (unsigned)__reduce_add_sync(0xFFFFFFFFu, n) * (unsigned)units;
         share = (int)((total + gridDim.x - 1) / gridDim.x);
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnGeom<TYPE, DP, MB>::CTAS) att
             seq0 = s_pref[s] * units;
         }
         AttnSeq sq;
-        sq.set<TILE>(len, p);
+        sq.set<TILE, NW>(len, p);
         const int unit = (int)((unsigned)(x - seq0) / (unsigned)length);
         const int h = p.n_rb == 1 ? unit : unit / p.n_rb, rb = unit - h * p.n_rb;        // a head's row blocks follow each other: the cache is in L2
         const int seg0 = seq0 + unit * length, seg1 = seg0 + length;
@@ -1153,7 +1155,7 @@ static __global__ void __launch_bounds__(ATT_SCORE_THREADS) attn_score_kernel(co
 {
     const int s = blockIdx.z, h = blockIdx.y;
     AttnSeq sq;
-    sq.set<ATT_MIN_TILE>(attn_len(p, s), p);
+    sq.set<ATT_MIN_TILE, ATT_MIN_NW>(attn_len(p, s), p);
     const int64_t sh = (int64_t)s * p.n_kv + h;
     const float4 *st = reinterpret_cast<const float4 *>(p.stats + 2 * sh * p.raw_rows);      // of two rows
     bool waited = false;
@@ -1194,7 +1196,7 @@ static cudaError_t launch_attn_mb(const AttnParams &p, int sms, int64_t steps, c
     using G = AttnGeom<TYPE, DP, MB>;
     static SmemCfg configured;
     const int most = sms * G::CTAS < ATT_MAX_CTAS ? sms * G::CTAS : ATT_MAX_CTAS;
-    return launch_with(attn_decode_kernel<TYPE, DP, MB>, configured, p, dim3((unsigned)(steps < most ? steps : most)), G::SMEM, st, false, false, ATT_THREADS);
+    return launch_with(attn_decode_kernel<TYPE, DP, MB>, configured, p, dim3((unsigned)(steps < most ? steps : most)), G::SMEM, st, false, false, G::THREADS);
 }
 
 template <int TYPE>
