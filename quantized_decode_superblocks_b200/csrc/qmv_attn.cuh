@@ -8,8 +8,8 @@
 // Two parts (m, l, o) of one row join as m = max, l and o scaled by 2^(m_i - m)
 // and added; out = o / l.
 //
-// Work split.  The cache is cut into tiles of 16 slots of one kv head, 4 of them
-// (one per warp) are a step.  The steps of all sequences, heads and row blocks
+// Work split.  The cache is cut into tiles of 16 or 32 slots of one kv head, one per
+// warp of a CTA is a step.  The steps of all sequences, heads and row blocks
 // are numbered through, and CTA c takes the c-th equal range of them, so that ragged batches and single long
 // sequences load every SM alike; the lengths are only known on the device, so
 // every CTA finds its own range from a prefix sum over them.  A (sequence, row
@@ -18,7 +18,7 @@
 // Two CTAs share an SM where shared memory allows, so that one streams while
 // the other starts or joins a segment.
 //
-// In a CTA, each of 4 warps streams every 4th tile through a ring of its own
+// In a CTA, each of 4 (6) warps streams every 4th (6th) tile through a ring of its own
 // (cp.async, NST stages) and multiplies on the tensor cores (m16n8k16, f32
 // accumulation) with the cache as the A operand:
 //   S^T[16 slots][8 rows] = K q^T,   O^T[16 dims][8 rows] += V^T P^T,
@@ -39,9 +39,9 @@
 // more than a slack, so most tiles need no reduction across lanes.
 //
 // Slots that no query of the call sees are not loaded (their shared memory is
-// zeroed by the copy).  A slot that only some of several queries see is kept out of
-// the others' results by zeroing its V operand per query, not by a zero
-// weight, since 0 * NaN is NaN.
+// zeroed by the copy).  A slot that only some of several queries see has weight 0
+// for the others; 0 * NaN is NaN, so in tiles with such slots NaN and infinities
+// among the values (Q8_0: the scales) are made finite first.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -240,6 +240,19 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint3
     const uint32_t vx = __float_as_uint(rx), vy = __float_as_uint(ry);
     mid = __byte_perm(vx, vy, 0x7632);
     lo = __byte_perm(__float_as_uint(rx - __uint_as_float(vx & 0xFFFF0000u)), __float_as_uint(ry - __uint_as_float(vy & 0xFFFF0000u)), 0x7632);
+}
+// A pair of 16-bit values brought within the type's finite range; NaN becomes its
+// lowest value (minimum and maximum return the operand that is a number).
+template <int TYPE>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t x)
+{
+    if constexpr (TYPE == KV_F16) {
+        const __half2 top = __half2half2(__ushort_as_half(0x7BFF)), y = __hmin2(__hmax2(*reinterpret_cast<const __half2 *>(&x), __hneg2(top)), top);
+        return *reinterpret_cast<const uint32_t *>(&y);
+    } else {
+        const __nv_bfloat162 top = __bfloat162bfloat162(__ushort_as_bfloat16(0x7F7F)), y = __hmin2(__hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&x), __hneg2(top)), top);
+        return *reinterpret_cast<const uint32_t *>(&y);
+    }
 }
 // (a, b) += (x, y), *= (x, y), += (x, y) * f: one instruction each.
 __device__ __forceinline__ void add2(float &a, float &b, float x, float y)
@@ -934,12 +947,16 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
                         for (int u = 0; u < SUB; ++u)
                             if (k < NPP - 1 || u > 0) mma_16<PBF>(t, r[u], pb[nb][u][k][0], pb[nb][u][k][1]);
                 };
-                if (!mixed) {
+                auto values = [&](auto &&each) {
 #pragma unroll
                     for (int i = 0; i < DP / 16; ++i) {
                         uint32_t r[SUB][4];
 #pragma unroll
-                        for (int u = 0; u < SUB; ++u) ldsm4t(r[u], va + G::at(16 * u + v_row, 2 * i + v_chunk));
+                        for (int u = 0; u < SUB; ++u) {
+                            ldsm4t(r[u], va + G::at(16 * u + v_row, 2 * i + v_chunk));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) each(r[u][k]);
+                        }
 #pragma unroll
                         for (int nb = 0; nb < MB; ++nb) {
                             float t[4];
@@ -948,38 +965,9 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
                             add2(acc[nb][i][2], acc[nb][i][3], t[2], t[3]);
                         }
                     }
-                } else {
-                    // query by query, the values it does not see as zeros
-                    const int tk1 = (min(row0 + G::ROWS, p.rows) - 1) / p.group;
-                    for (int tk = row0 / p.group; tk <= tk1; ++tk) {
-                        const int at = sq.first + tk;
-                        uint32_t z[SUB][2];                               // of slots 2 c4, 2 c4 + 1 and + 8
-#pragma unroll
-                        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int j = j0 + 16 * u + 8 * i + 2 * c4;
-                                z[u][i] = (attn_sees(p, at, j) ? 0xFFFFu : 0u) | (attn_sees(p, at, j + 1) ? 0xFFFF0000u : 0u);
-                            }
-#pragma unroll
-                        for (int i = 0; i < DP / 16; ++i) {
-                            uint32_t r[SUB][4];
-#pragma unroll
-                            for (int u = 0; u < SUB; ++u) {
-                                ldsm4t(r[u], va + G::at(16 * u + v_row, 2 * i + v_chunk));
-                                r[u][0] &= z[u][0]; r[u][1] &= z[u][0]; r[u][2] &= z[u][1]; r[u][3] &= z[u][1];
-                            }
-#pragma unroll
-                            for (int nb = 0; nb < MB; ++nb) {
-                                float t[4];
-                                product(t, r, nb);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (s_at[nb * 8 + 2 * c4 + (e & 1)] == at) acc[nb][i][e] += t[e];
-                            }
-                        }
-                    }
-                }
+                };
+                if (mixed) values([](uint32_t &x) { x = finite_pair<TYPE>(x); });
+                else values([](uint32_t &) {});
             }
         }
         cp_wait<0>();
