@@ -328,7 +328,8 @@ typedef struct {
  *   angle = pos * inv_freq[i], i < rope_dim / 2;  a' = a cos - b sin,
  *   b' = a sin + b cos for every pair (a, b) of the first rope_dim values of
  *   every q and k head (angles, sine and cosine in 64 bits, so that far
- *   positions keep their phase; rounded once to f32, then to the cache's type)
+ *   positions keep their phase; the sums with 48 bits of either, rounded once
+ *   to f32, then to the cache's type)
  *   Q8_0 blocks: scale = f16(min(amax / 127, 65504)), quant = value / scale
  *   rounded to even and clamped to +-127, 0 where the scale is 0.
  * Token t (0 <= t < n_tok) of sequence s goes to slot kv_len[s] - n_tok + t

@@ -14,13 +14,24 @@ namespace qmv {
 // few KB per token: bound by launch and memory latency, not by bandwidth.
 constexpr int APP_THREADS = 128, APP_CTAS = 4;     // CTAs on a SM
 
-// Sine and cosine of pos * f.  The angle is brought within one turn by k turns
+// Cosine and sine of pos * f, each as two floats (48 bits).  The angle is brought within one turn by k turns
 // taken away in two parts (Cody and Waite), exact to 2^-53 of a turn for any
 // 31-bit position, so that the library's function never takes its long path.
-__device__ __forceinline__ void rope_sincos(double pos, float f, double *s, double *c)
+__device__ __forceinline__ float4 rope_turn(double pos, float f)
 {
     const double a = pos * (double)f, k = rint(a * 0.15915494309189535);
-    sincos(fma(-k, 2.4492935982947064e-16, fma(-k, 6.283185307179586, a)), s, c);
+    double sn, c;
+    sincos(fma(-k, 2.4492935982947064e-16, fma(-k, 6.283185307179586, a)), &sn, &c);
+    const float ch = (float)c, sh = (float)sn;
+    return make_float4(ch, (float)(c - ch), sh, (float)(sn - sh));
+}
+
+// a c + b s, rounded once: the products' and the sum's roundings are caught in f32.
+__device__ __forceinline__ float rope_sum(float a, float b, float4 t)
+{
+    const float p = a * t.x, q = b * t.z, r = p + q, v = r - p;
+    const float left = fmaf(a, t.y, fmaf(a, t.x, -p)) + fmaf(b, t.w, fmaf(b, t.z, -q));
+    return r + (((p - (r - v)) + (q - v)) + left);
 }
 
 struct AppendParams {
@@ -37,9 +48,12 @@ struct AppendParams {
     int *err;
 };
 
+// NB: values of a head per lane, 32 apart.  A lane's partners and turns are the
+// same for every head and stay in registers.
+template <int NB>
 static __global__ void __launch_bounds__(APP_THREADS, APP_CTAS) kv_append_kernel(const __grid_constant__ AppendParams p)
 {
-    __shared__ double s_cos[128], s_sin[128];
+    __shared__ float4 s_turn[16 * NB];             // cosine and sine, each as a float and what it leaves
     __shared__ long long s_at;                     // the slot's first element, -1: nothing to store
     const int tok = blockIdx.x, s = tok / p.n_tok, t = tok % p.n_tok;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -54,56 +68,73 @@ static __global__ void __launch_bounds__(APP_THREADS, APP_CTAS) kv_append_kernel
         if (raw != len) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
         s_at = at;
     }
-    const int nb = (p.dim + 31) / 32, nq = p.q_out ? p.n_head : 0, heads = nq + 2 * p.n_kv;
+    const int nq = p.q_out ? p.n_head : 0, heads = nq + 2 * p.n_kv;
     const int half = p.rope_dim / 2, step = gridDim.y * (APP_THREADS / 32);
-    int head = blockIdx.y * (APP_THREADS / 32) + warp;
-    float y[8], z[8];                              // this lane's values and their partners
+    auto second = [&](int d) { return p.rope_pairs ? d & 1 : d >= half; };          // of its pair
+    int head = blockIdx.y * (APP_THREADS / 32) + warp, partner[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int d = b * 32 + lane;
+        partner[b] = d >= p.rope_dim ? -1 : p.rope_pairs ? d ^ 1 : d < half ? d + half : d - half;
+    }
+    float y[NB], z[NB];                            // this lane's values and their partners
     auto load = [&]() {
         if (head >= heads) return;
-        const bool is_q = head < nq, is_k = !is_q && head < nq + p.n_kv;
-        const int h = is_q ? head : is_k ? head - nq : head - nq - p.n_kv;
-        const float *x = is_q ? p.q_in + tok * p.q_stride : is_k ? p.k_in + tok * p.k_stride : p.v_in + tok * p.v_stride;
-        x += (int64_t)h * p.dim;
+        const float *x = head < nq ? p.q_in + tok * p.q_stride + (int64_t)head * p.dim
+                         : head < nq + p.n_kv ? p.k_in + tok * p.k_stride + (int64_t)(head - nq) * p.dim
+                                              : p.v_in + tok * p.v_stride + (int64_t)(head - nq - p.n_kv) * p.dim;
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-            const int d = b * 32 + lane;
-            y[b] = b < nb && d < p.dim ? x[d] : 0.f;
-            z[b] = !is_q && !is_k ? 0.f : d < p.rope_dim ? x[p.rope_pairs ? d ^ 1 : d < half ? d + half : d - half] : 0.f;
+        for (int b = 0; b < NB; ++b) y[b] = b * 32 + lane < p.dim ? x[b * 32 + lane] : 0.f;
+        if (head < nq + p.n_kv) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) z[b] = partner[b] >= 0 ? x[partner[b]] : 0.f;
         }
     };
     load();
     const double pos = p.pos ? __ldg(p.pos + tok) : slot;
-    for (int i = threadIdx.x; i < half; i += APP_THREADS) rope_sincos(pos, __ldg(p.inv_freq + i), s_sin + i, s_cos + i);
+    for (int i = threadIdx.x; i < half; i += APP_THREADS) s_turn[i] = rope_turn(pos, __ldg(p.inv_freq + i));
     __syncthreads();
     const long long at = s_at;
-    for (; head < heads; head += step, load()) {
-        const bool is_q = head < nq, is_k = !is_q && head < nq + p.n_kv;
-        const int h = is_q ? head : is_k ? head - nq : head - nq - p.n_kv;
-        __syncwarp();                              // q may be rotated in place: all is read before anything is written
+    float4 turn[NB];
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-            if (b >= nb) break;
-            const int d = b * 32 + lane;
-            const bool in = d < p.dim;
-            float w = y[b];
-            if ((is_q || is_k) && d < p.rope_dim) {
-                const int i = p.rope_pairs ? d >> 1 : d < half ? d : d - half;
-                const bool second = p.rope_pairs ? d & 1 : d >= half;
-                const double own = y[b], other = z[b];
-                w = (float)(second ? other * s_sin[i] + own * s_cos[i] : own * s_cos[i] - other * s_sin[i]);
-            }
-            if (is_q) {
-                if (in) p.q_out[tok * p.q_out_stride + (int64_t)h * p.dim + d] = w;
-                continue;
-            }
-            if (at < 0) continue;
-            const long long e = at + h * p.head_stride + d;
-            uint8_t *pool = is_k ? p.k : p.v;
+    for (int b = 0; b < NB; ++b) {
+        const int d = b * 32 + lane;
+        if (partner[b] < 0) continue;
+        turn[b] = s_turn[p.rope_pairs ? d >> 1 : d < half ? d : d - half];
+        if (!second(d)) {                          // a cos - b sin
+            turn[b].z = -turn[b].z;
+            turn[b].w = -turn[b].w;
+        }
+    }
+    for (; head < heads; head += step, load()) {
+        __syncwarp();                              // q may be rotated in place: all is read before anything is written
+        if (head < nq + p.n_kv) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                if (partner[b] >= 0) y[b] = rope_sum(y[b], z[b], turn[b]);
+        }
+        if (head < nq) {
+            float *o = p.q_out + tok * p.q_out_stride + (int64_t)head * p.dim;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                if (b * 32 + lane < p.dim) o[b * 32 + lane] = y[b];
+            continue;
+        }
+        if (at < 0) continue;
+        const bool is_k = head < nq + p.n_kv;
+        const int h = is_k ? head - nq : head - nq - p.n_kv;
+        const long long e0 = at + h * p.head_stride + lane;
+        uint8_t *pool = is_k ? p.k : p.v;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const bool in = b * 32 + lane < p.dim;
+            const long long e = e0 + b * 32;
             if (p.type == KV_F16) {
-                if (in) reinterpret_cast<__half *>(pool)[e] = __float2half_rn(w);
+                if (in) reinterpret_cast<__half *>(pool)[e] = __float2half_rn(y[b]);
             } else if (p.type == KV_BF16) {
-                if (in) reinterpret_cast<__nv_bfloat16 *>(pool)[e] = __float2bfloat16_rn(w);
-            } else {
+                if (in) reinterpret_cast<__nv_bfloat16 *>(pool)[e] = __float2bfloat16_rn(y[b]);
+            } else if (b * 32 < p.dim) {
+                const float w = y[b];
                 float mx = fabsf(w);
                 for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
                 const __half dh = __float2half_rn(fminf(__fdiv_rn(mx, 127.f), 65504.f));

@@ -254,7 +254,11 @@ int kv_append(const qmv_append *a, qmv_stream_t stream)
     const int tokens = a->n_seq * a->n_tok;
     const int heads = (a->q ? a->n_head : 0) + 2 * c.n_kv_head;
     const int gy = (int)std::min<int64_t>(ceil_div(heads, APP_THREADS / 32), std::max(1, APP_CTAS * di.sm_count / tokens));
-    kv_append_kernel<<<dim3((unsigned)tokens, (unsigned)gy), APP_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    const dim3 grid((unsigned)tokens, (unsigned)gy);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (c.head_dim <= 64) kv_append_kernel<2><<<grid, APP_THREADS, 0, st>>>(p);
+    else if (c.head_dim <= 128) kv_append_kernel<4><<<grid, APP_THREADS, 0, st>>>(p);
+    else kv_append_kernel<8><<<grid, APP_THREADS, 0, st>>>(p);
     return finish(cudaGetLastError());
 }
 
