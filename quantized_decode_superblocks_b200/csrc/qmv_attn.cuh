@@ -44,6 +44,8 @@
 // among the values (Q8_0: the scales) are made finite first.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "qmv_device.cuh"
@@ -89,6 +91,7 @@ struct AttnParams {
     int32_t page_size, page_shift, max_len;              // page_shift < 0: not a power of two
     int32_t mb, n_rb;                                    // 8-row blocks of a CTA, row blocks of a head
     int32_t window, n_sink;
+    float inv_group;                                     // 1 / group: row / group of up to 1024 rows by a product
     float scale_log2, l_shift;                           // l counts 2^l_shift times the weights
     unsigned *counters;                                  // [ATT_MAX_CTAS], zero between calls
     float *part_ml, *part_o;                             // [2 * CTAs][8 mb][2], [..][dim]
@@ -140,6 +143,9 @@ __device__ __forceinline__ int attn_len(const AttnParams &p, int s)
     const int n = __ldg(p.kv_len + s);
     return min(max(n, 0), p.max_len);
 }
+
+// row / group: (row + 1/2) / group is at least 1 / 2048 from a whole number, the product's error below 2^-13
+__device__ __forceinline__ int attn_token(const AttnParams &p, int row) { return (int)(((float)row + 0.5f) * p.inv_group); }
 
 __device__ __forceinline__ bool attn_sees(const AttnParams &p, int at, int j)
 {
@@ -402,7 +408,7 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
         q.set<TILE, NW>(my_len, p);
         const int n = lane < p.n_seq ? q.n_steps : 0;
         total = (unsigned)__reduce_add_sync(0xFFFFFFFFu, n) * (unsigned)units;
-        share = (int)((total + gridDim.x - 1) / gridDim.x);
+        share = total <= gridDim.x ? 1 : (int)((total + gridDim.x - 1) / gridDim.x);
         if (share > 1 && p.n_seq * units <= (int)gridDim.x) choose(reduce(ctas_of(n)));
         my_length = length_of(n);
         int x = my_length;
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
             if ((raw < 0 || raw > p.max_len) && blockIdx.x == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
             return steps_of(s);
         });
-        share = (int)((total + gridDim.x - 1) / gridDim.x);
+        share = total <= gridDim.x ? 1 : (int)((total + gridDim.x - 1) / gridDim.x);
         if (share > 1 && p.n_seq * units <= (int)gridDim.x) {
             int4 n = make_int4(0, 0, 0, 0);
             for (int s = tid; s < p.n_seq; s += NT) {
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
         const int q_nb = G::QREG ? 0 : warp;
         float qraw[Q_EARLY ? DP / 16 : 1][4];
         auto q_row = [&](int row) {
-            const int tok = row < p.rows ? row / p.group : 0;
+            const int tok = row < p.rows ? attn_token(p, row) : 0;
             return p.q + (int64_t)(s * p.n_tok + tok) * p.q_stride + (int64_t)(h * p.group + (row < p.rows ? row - tok * p.group : 0)) * p.dim;
         };
         auto q_load4 = [&](const float *x, bool row_ok, int ks, float (&f)[4]) {
@@ -631,7 +637,7 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
             }
             return sf;
         };
-        for (int r = tid; r < G::ROWS; r += NT) s_at[r] = row0 + r < p.rows ? sq.first + (row0 + r) / p.group : -1;
+        for (int r = tid; r < G::ROWS; r += NT) s_at[r] = row0 + r < p.rows ? sq.first + attn_token(p, row0 + r) : -1;
         float sf[MB][2];                                                  // of rows 2 c4, 2 c4 + 1 of every block
         if constexpr (G::QREG) {
             const float f = q_block(0, [&](int ks, const uint32_t (&w)[QW]) {
@@ -1052,16 +1058,16 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
         }
         if (!whole) {
             // ---- the last CTA of the segment joins its parts, in CTA order
-            const int cta0 = (int)((unsigned)seg0 / (unsigned)share), cta1 = (int)((unsigned)(seg1 - 1) / (unsigned)share), n = cta1 - cta0 + 1;
+            const int cta0 = share == 1 ? seg0 : (int)((unsigned)seg0 / (unsigned)share), cta1 = share == 1 ? seg1 - 1 : (int)((unsigned)(seg1 - 1) / (unsigned)share), n = cta1 - cta0 + 1;
             __syncthreads();
             if (tid == 0) s_last = atomic_inc_acq_rel(p.counters + cta0) == (unsigned)(n - 1);
             __syncthreads();
             if (s_last) {
                 if (tid == 0) p.counters[cta0] = 0u;
-                constexpr int CH = 16;                                    // parts in flight
                 // part c: the second of CTA cta0's two slots for c = 0, else the first of CTA cta0 + c's
                 const int64_t po_step = (int64_t)G::ROWS * p.dim;
-                auto join = [&](int r, int d, int c_first, int c_step, float4 &v, float &mr, float &lr) {
+                auto join = [&](auto in_flight, int r, int d, int c_first, int c_step, float4 &v, float &mr, float &lr) {
+                    constexpr int CH = decltype(in_flight)::value;        // parts in flight
                     const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + (int64_t)2 * cta0 * G::ROWS + r;
                     const float *po = p.part_o + ((int64_t)2 * cta0 * G::ROWS + r) * p.dim + 4 * d;
                     v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1097,13 +1103,13 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
                 };
                 float4 v;
                 float mr, lr;
-                if (nrow * D4 <= NT / 2 && n > CH) {                      // many parts of few rows: two threads take every other one
+                if (nrow * D4 <= NT / 2 && n > 16) {                      // many parts of few rows: two threads take every other one
                     float4 *sv = reinterpret_cast<float4 *>(smem);
                     float2 *sm = reinterpret_cast<float2 *>(smem + NT / 2 * sizeof(float4));
                     const int half = tid / (NT / 2), i = tid % (NT / 2), r = i / D4, d = i % D4;
                     const bool in = i < nrow * D4 && 4 * d < p.dim;
                     if (in) {
-                        join(r, d, half, 2, v, mr, lr);
+                        join(std::integral_constant<int, 16>(), r, d, half, 2, v, mr, lr);
                         if (half) {
                             sv[i] = v;
                             sm[i] = make_float2(mr, lr);
@@ -1122,7 +1128,8 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
                     for (int i = tid; i < nrow * D4; i += NT) {
                         const int r = i / D4, d = i % D4;
                         if (4 * d >= p.dim) continue;
-                        join(r, d, 0, 1, v, mr, lr);
+                        if (n <= 8) join(std::integral_constant<int, 8>(), r, d, 0, 1, v, mr, lr);
+                        else join(std::integral_constant<int, 16>(), r, d, 0, 1, v, mr, lr);
                         put(r, d, v, lr);
                         if (d == 0) put_stats(r, mr, lr);
                     }

@@ -164,6 +164,7 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     p.n_kv = c.n_kv_head;
     p.group = a->n_head / c.n_kv_head;
     p.rows = p.group * p.n_tok;
+    p.inv_group = 1.f / (float)p.group;
     p.dim = c.head_dim;
     p.page_size = c.page_size;
     p.page_shift = page_shift(c.page_size);
