@@ -144,6 +144,14 @@ __device__ __forceinline__ int attn_len(const AttnParams &p, int s)
     return min(max(n, 0), p.max_len);
 }
 
+// a / b where the quotient is below 2^20: the product with the reciprocal is off by at most one.
+__device__ __forceinline__ int div_small(int a, int b)
+{
+    int q = (int)(__fdividef((float)a, (float)b));
+    const int left = a - q * b;
+    q += left < 0 ? -1 : left >= b ? 1 : 0;
+    return q;
+}
 // row / group: (row + 1/2) / group is at least 1 / 2048 from a whole number, the product's error below 2^-13
 __device__ __forceinline__ int attn_token(const AttnParams &p, int row) { return (int)(((float)row + 0.5f) * p.inv_group); }
 
@@ -391,13 +399,13 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
         if (padded) share += more;
     };
     auto ctas_of = [&](int n) {
-        const unsigned k = (unsigned)n - 1u, d = (unsigned)share;
-        return n == 0 ? make_int4(0, 0, 0, 0) : make_int4(k / d + 1u, k / (d + 1u) + 1u, k / (d + 2u) + 1u, k / (d + 3u) + 1u);
+        const int k = n - 1;
+        return n == 0 ? make_int4(0, 0, 0, 0) : make_int4(div_small(k, share) + 1, div_small(k, share + 1) + 1, div_small(k, share + 2) + 1, div_small(k, share + 3) + 1);
     };
     auto reduce = [&](int4 n) {
         return make_int4(__reduce_add_sync(0xFFFFFFFFu, n.x), __reduce_add_sync(0xFFFFFFFFu, n.y), __reduce_add_sync(0xFFFFFFFFu, n.z), __reduce_add_sync(0xFFFFFFFFu, n.w));
     };
-    auto length_of = [&](int n) { return padded ? (int)((unsigned)(n + share - 1) / (unsigned)share) * share : n; };
+    auto length_of = [&](int n) { return padded ? div_small(n + share - 1, share) * share : n; };
     const bool few = p.n_seq <= 32;                                       // sequences: one a lane, every warp by itself
     int my_len = 0, my_length = 0, my_pref = 0;
     if (few) {
@@ -475,8 +483,8 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
         }
         AttnSeq sq;
         sq.set<TILE, NW>(len, p);
-        const int unit = (int)((unsigned)(x - seq0) / (unsigned)length);
-        const int h = p.n_rb == 1 ? unit : unit / p.n_rb, rb = unit - h * p.n_rb;        // a head's row blocks follow each other: the cache is in L2
+        const int unit = div_small(x - seq0, length);
+        const int h = p.n_rb == 1 ? unit : div_small(unit, p.n_rb), rb = unit - h * p.n_rb;        // a head's row blocks follow each other: the cache is in L2
         const int seg0 = seq0 + unit * length, seg1 = seg0 + length;
         const int row0 = rb * G::ROWS;
         const int tile0 = (x - seg0) * NW + warp;                         // this warp's first tile
@@ -1039,10 +1047,11 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
         constexpr int D4 = DP / 4;                                        // a thread takes 4 dims of a row
         auto put = [&](int r, int d, float4 v, float lr) {
             float *o = out_row(r) + 4 * d;
-            o[0] = lr != 0.f ? v.x / lr : 0.f;
-            o[1] = lr != 0.f ? v.y / lr : 0.f;
-            o[2] = lr != 0.f ? v.z / lr : 0.f;
-            o[3] = lr != 0.f ? v.w / lr : 0.f;
+            const float f = lr != 0.f ? __frcp_rn(lr) : 0.f;
+            o[0] = v.x * f;
+            o[1] = v.y * f;
+            o[2] = v.z * f;
+            o[3] = v.w * f;
         };
         for (int i = tid; i < nrow * D4; i += NT) {
             const int r = i / D4, d = i % D4;
@@ -1058,7 +1067,7 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
         }
         if (!whole) {
             // ---- the last CTA of the segment joins its parts, in CTA order
-            const int cta0 = share == 1 ? seg0 : (int)((unsigned)seg0 / (unsigned)share), cta1 = share == 1 ? seg1 - 1 : (int)((unsigned)(seg1 - 1) / (unsigned)share), n = cta1 - cta0 + 1;
+            const int cta0 = div_small(seg0, share), cta1 = div_small(seg1 - 1, share), n = cta1 - cta0 + 1;
             __syncthreads();
             if (tid == 0) s_last = atomic_inc_acq_rel(p.counters + cta0) == (unsigned)(n - 1);
             __syncthreads();
