@@ -8,6 +8,9 @@
 
 namespace qmv {
 
+template <class Params>
+__device__ __forceinline__ int page_of(int slot, const Params &p) { return p.page_shift >= 0 ? slot >> p.page_shift : slot / p.page_size; }
+
 // -------------------------------------------------------------- append --
 // One CTA per (token, share of the heads): the token's cosines and sines once
 // in 64 bits, then one warp per head, whose first head is loaded meanwhile.  A
@@ -41,7 +44,7 @@ struct AppendParams {
     float *q_out;
     int64_t q_stride, k_stride, v_stride, q_out_stride;
     int32_t type, n_head, n_kv, dim, n_tok, rope_dim, rope_pairs;
-    int32_t page_size, max_len;
+    int32_t page_size, page_shift, max_len;          // page_shift < 0: not a power of two
     const int32_t *table, *kv_len, *pos;
     int64_t table_stride;
     const float *inv_freq;
@@ -55,23 +58,23 @@ static __global__ void __launch_bounds__(APP_THREADS, APP_CTAS) kv_append_kernel
 {
     __shared__ float4 s_turn[16 * NB];             // cosine and sine, each as a float and what it leaves
     __shared__ long long s_at;                     // the slot's first element, -1: nothing to store
-    const int tok = blockIdx.x, s = tok / p.n_tok, t = tok % p.n_tok;
+    const int t = blockIdx.x, s = blockIdx.y, tok = s * p.n_tok + t;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int raw = __ldg(p.kv_len + s), len = min(max(raw, 0), p.max_len), slot = len - p.n_tok + t;
     if (threadIdx.x == 0) {
         long long at = -1;
         if (slot >= 0) {
-            const int page = __ldg(p.table + (int64_t)s * p.table_stride + slot / p.page_size);
-            if (page >= 0 && page < p.n_pages) at = page * p.page_stride + (slot % p.page_size) * p.slot_stride;
+            const int i = page_of(slot, p), page = __ldg(p.table + (int64_t)s * p.table_stride + i);
+            if (page >= 0 && page < p.n_pages) at = page * p.page_stride + (slot - i * p.page_size) * p.slot_stride;
             else atomicOr(p.err, 8 /* QMV_DEVERR_PAGE_ID */);
         }
         if (raw != len) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
         s_at = at;
     }
     const int nq = p.q_out ? p.n_head : 0, heads = nq + 2 * p.n_kv;
-    const int half = p.rope_dim / 2, step = gridDim.y * (APP_THREADS / 32);
+    const int half = p.rope_dim / 2, step = gridDim.z * (APP_THREADS / 32);
     auto second = [&](int d) { return p.rope_pairs ? d & 1 : d >= half; };          // of its pair
-    int head = blockIdx.y * (APP_THREADS / 32) + warp, partner[NB];
+    int head = blockIdx.z * (APP_THREADS / 32) + warp, partner[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const int d = b * 32 + lane;
@@ -179,7 +182,7 @@ struct EvictParams {
     int64_t score_stride, score_out_stride, table_stride, dst_table_stride;
     const int32_t *table, *kv_len, *dst_table;
     int32_t *kept, *len_out;
-    int32_t n_kv, page_size, max_len, keep_first, keep_last, budget;
+    int32_t n_kv, page_size, page_shift, max_len, keep_first, keep_last, budget;
     int32_t row_bytes, scale_words, eb;       // of one slot and head; scale_words: 4-byte words of its scales
     int *err;
 };
@@ -343,7 +346,7 @@ static __global__ void __launch_bounds__(EV_COPY_THREADS) kv_evict_copy_kernel(c
     const int m = min(min(max(__ldg(p.kv_len + s), 0), p.max_len), p.budget);
     const int i = (blockIdx.x / p.n_kv * (EV_COPY_THREADS / 32) + warp) * EV_SLOTS + lane % EV_SLOTS;
     const bool in = lane < 2 * EV_SLOTS && i < m;
-    const int pd = in ? __ldg(p.dst_table + (int64_t)s * p.dst_table_stride + i / p.page_size) : -1;
+    const int di = page_of(i, p), pd = in ? __ldg(p.dst_table + (int64_t)s * p.dst_table_stride + di) : -1;
     const uint32_t bar = smem_addr(s_bar + warp);
     if (lane == 0) {
         mbar_init(bar, 1);
@@ -354,11 +357,11 @@ static __global__ void __launch_bounds__(EV_COPY_THREADS) kv_evict_copy_kernel(c
     bool ok = false;
     if (in) {
         const int j = __ldcg(p.kept + ((int64_t)s * p.n_kv + h) * p.budget + i);
-        const int ps = __ldg(p.table + (int64_t)s * p.table_stride + j / p.page_size);
+        const int si = page_of(j, p), ps = __ldg(p.table + (int64_t)s * p.table_stride + si);
         ok = ps >= 0 && ps < p.n_pages && pd >= 0 && pd < p.n_pages;
         if (!ok) atomicOr(p.err, 8 /* QMV_DEVERR_PAGE_ID */);
-        es = ps * p.page_stride + h * p.head_stride + (j % p.page_size) * p.slot_stride;
-        ed = pd * p.page_stride + h * p.head_stride + (i % p.page_size) * p.slot_stride;
+        es = ps * p.page_stride + h * p.head_stride + (j - si * p.page_size) * p.slot_stride;
+        ed = pd * p.page_stride + h * p.head_stride + (i - di * p.page_size) * p.slot_stride;
     }
     const uint32_t n_ok = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, ok)), rb = (uint32_t)p.row_bytes;
     if (n_ok == 0) return;

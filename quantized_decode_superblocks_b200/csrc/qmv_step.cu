@@ -245,6 +245,7 @@ int kv_append(const qmv_append *a, qmv_stream_t stream)
     p.rope_dim = a->rope_dim;
     p.rope_pairs = a->rope_style == QMV_ROPE_PAIRS;
     p.page_size = c.page_size;
+    p.page_shift = page_shift(c.page_size);
     p.max_len = (int)slots;
     p.table = a->block_table;
     p.kv_len = a->kv_len;
@@ -255,7 +256,7 @@ int kv_append(const qmv_append *a, qmv_stream_t stream)
     const int tokens = a->n_seq * a->n_tok;
     const int heads = (a->q ? a->n_head : 0) + 2 * c.n_kv_head;
     const int gy = (int)std::min<int64_t>(ceil_div(heads, APP_THREADS / 32), std::max(1, APP_CTAS * di.sm_count / tokens));
-    const dim3 grid((unsigned)tokens, (unsigned)gy);
+    const dim3 grid((unsigned)a->n_tok, (unsigned)a->n_seq, (unsigned)gy);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (c.head_dim <= 64) kv_append_kernel<2><<<grid, APP_THREADS, 0, st>>>(p);
     else if (c.head_dim <= 128) kv_append_kernel<4><<<grid, APP_THREADS, 0, st>>>(p);
@@ -308,6 +309,7 @@ int kv_evict(const qmv_evict *a, qmv_stream_t stream)
     p.len_out = a->len_out;
     p.n_kv = c.n_kv_head;
     p.page_size = c.page_size;
+    p.page_shift = page_shift(c.page_size);
     p.max_len = (int)std::min(slots, a->score_stride);
     p.keep_first = a->keep_first;
     p.keep_last = a->keep_last;
