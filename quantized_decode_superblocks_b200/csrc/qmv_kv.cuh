@@ -2,6 +2,7 @@
 // cache for each sequence (kv_evict); both declared in include/qmv.h.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "qmv_attn.cuh"
@@ -161,9 +162,13 @@ static __global__ void __launch_bounds__(APP_THREADS, APP_CTAS) kv_append_kernel
 // leaves no slot undecided is the last one: scores that all differ need two.
 // Then each warp writes the kept slots of its part in order, at the place that
 // the counts of the warps before it give: one cache of 4352 slots 5 us, 16 of
-// up to 16384 slots 11 us, bound by the instructions of one SM per head.  (Spread over
-// a cluster of 8 CTAs, whose counts went through distributed shared memory:
-// 12 us, and 18 us in each of three waves.)
+// up to 16384 slots 11 us, bound by the instructions of one SM per head.
+// Long caches of few heads: a cluster of EV_CL CTAs per head, each for a part of
+// the slots.  A CTA adds up the cluster's counts of its share of the digits over
+// distributed shared memory, and only the shares' sums and the chosen digit go
+// to all (every CTA reading all counts took 5 us a round).  One cache, 8 heads,
+// choice and copy: 10000 slots 19 us instead of 15 us, 20000 slots 20
+// instead of 21 us, 131072 slots 35 instead of 164 us.
 //
 // Copy: a warp per EV_SLOTS kept slots of a (sequence, head), the heads of the
 // same slots next to each other; 16 x 8 heads x 4096 slots of 512 bytes, in and
@@ -172,7 +177,11 @@ static __global__ void __launch_bounds__(APP_THREADS, APP_CTAS) kv_append_kernel
 // many a lane has in flight.)
 constexpr int EV_THREADS = 1024, EV_BINS = 2048;
 constexpr int EV_KEYS = 40960;                // keys that shared memory holds; those of later slots are made anew in every round
+constexpr int EV_CL = 8;                      // CTAs of a head, long caches
 constexpr int EV_COPY_THREADS = 128, EV_SLOTS = 16;     // slots: of a warp of the copy
+
+// Whether several CTAs choose for each head.
+static inline bool evict_cluster(int max_len, int heads, int sms) { return max_len > 16384 && heads * EV_CL <= sms; }
 
 struct EvictParams {
     uint8_t *k, *v, *ks, *vs;
@@ -195,18 +204,24 @@ __device__ __forceinline__ uint32_t evict_key(float x)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-static __global__ void __launch_bounds__(EV_THREADS) kv_evict_kernel(const __grid_constant__ EvictParams p)
+// CL: CTAs of a (sequence, head), a cluster where more than one; CTA `rank` looks after the rank-th part of the slots.
+template <int CL>
+__device__ __forceinline__ void evict_choose(const EvictParams &p)
 {
+    namespace cg = cooperative_groups;
     constexpr int NW = EV_THREADS / 32, PER = EV_BINS / EV_THREADS, FLY = 8;      // FLY: loads of a thread in flight
     static_assert(NW == 32 && PER == 2, "one warp reads the warps' counts; a thread has two digits");
     __shared__ __align__(16) int s_hist[EV_BINS];
     __shared__ int s_sel[3];
     __shared__ int s_up[NW], s_eq[NW];
-    const int h = blockIdx.x, s = blockIdx.y;
+    __shared__ int s_all[CL], s_cnt[2];                                           // slots of every CTA's digits; this one's kept, and at the last key
+    const int rank = blockIdx.x % CL, h = blockIdx.x / CL, s = blockIdx.y;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");              // the copy, which waits for this kernel's end
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int raw = __ldg(p.kv_len + s), n = min(max(raw, 0), p.max_len), m = min(n, p.budget);
     if (raw != n && tid == 0) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
+    const int chunk = (int)(((int64_t)n + CL * EV_THREADS - 1) / (CL * EV_THREADS)) * 32;            // slots of a warp
+    const int a = (int)min((int64_t)n, (int64_t)rank * chunk * NW), b = (int)min((int64_t)n, (int64_t)a + (int64_t)chunk * NW);
     const int64_t sh = (int64_t)s * p.n_kv + h;
     const float *score = p.score + sh * p.score_stride;
     float *score_out = p.score_out + sh * p.score_out_stride;
@@ -214,29 +229,39 @@ static __global__ void __launch_bounds__(EV_THREADS) kv_evict_kernel(const __gri
     const int mid0 = min(p.keep_first, n), mid1 = max(mid0, n - p.keep_last);     // ranked slots
     const bool all = n <= p.budget;
 
-    extern __shared__ __align__(16) uint32_t s_key[];                             // [min(slots, EV_KEYS)], the largest for the kept ends
+    extern __shared__ __align__(16) uint32_t s_key[];                             // [min(slots, EV_KEYS)] of this CTA's, the largest for the kept ends
     auto key_at = [&](int j, float x) { return j < mid0 || j >= mid1 ? 0xFFFFFFFFu : evict_key(x); };
-    auto key_of = [&](int j) { return j < EV_KEYS ? s_key[j] : key_at(j, __ldg(score + j)); };
+    auto key_of = [&](int j) { return j - a < EV_KEYS ? s_key[j - a] : key_at(j, __ldg(score + j)); };
     uint32_t prefix = 0xFFFFFFFFu;            // no ranked key is that large
     int shift = 0, want = p.budget - p.keep_first - p.keep_last;                  // still to take within the prefix
     bool ties = false;                                                            // only some of the slots with the last key are kept
     if (!all) {
         reinterpret_cast<int2 *>(s_hist)[tid] = make_int2(0, 0);
         __syncthreads();
-        for (int64_t j0 = tid; j0 < n; j0 += FLY * EV_THREADS) {                  // keys, and the counts of their first digit
+        for (int64_t j0 = a + tid; j0 < b; j0 += FLY * EV_THREADS) {              // keys, and the counts of their first digit
             float x[FLY];
 #pragma unroll
-            for (int u = 0; u < FLY; ++u) x[u] = j0 + u * EV_THREADS < n ? __ldg(score + j0 + u * EV_THREADS) : 0.f;
+            for (int u = 0; u < FLY; ++u) x[u] = j0 + u * EV_THREADS < b ? __ldg(score + j0 + u * EV_THREADS) : 0.f;
 #pragma unroll
             for (int u = 0; u < FLY; ++u) {
                 const int64_t j = j0 + u * EV_THREADS;
-                if (j < n) {
+                if (j < b) {
                     const uint32_t key = key_at((int)j, x[u]);
-                    if (j < EV_KEYS) s_key[j] = key;
+                    if (j - a < EV_KEYS) s_key[j - a] = key;
                     if (key != 0xFFFFFFFFu) atomicAdd(s_hist + (key >> 21), 1);
                 }
             }
         }
+        auto sum_before = [&](int own) {                                          // over the threads before this one
+            int up = own;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, up, o);
+                if (lane >= o) up += y;
+            }
+            if (lane == 31) s_up[warp] = up;
+            __syncthreads();
+            return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s_up[lane] : 0) + up - own;
+        };
         for (int pass = 0; pass < 3 && want > 0; ++pass) {
             const int above = shift;                                              // the digits that are decided lie above this bit
             shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
@@ -245,31 +270,55 @@ static __global__ void __launch_bounds__(EV_THREADS) kv_evict_kernel(const __gri
                 reinterpret_cast<int2 *>(s_hist)[tid] = make_int2(0, 0);
                 __syncthreads();
 #pragma unroll 4
-                for (int64_t j = mid0 + tid; j < mid1; j += EV_THREADS) {
+                for (int64_t j = max(mid0, a) + tid; j < min(mid1, b); j += EV_THREADS) {
                     const uint32_t key = key_of((int)j);
                     if ((key >> above) == prefix) atomicAdd(s_hist + ((key >> shift) & digits), 1);
                 }
             }
-            __syncthreads();
-            // this thread's two digits, from the top down
-            const int lo = EV_BINS - PER * (tid + 1);
-            const int2 c = *reinterpret_cast<const int2 *>(s_hist + lo);
-            int up = c.x + c.y;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xFFFFFFFFu, up, o);
-                if (lane >= o) up += y;
+            if constexpr (CL == 1) {
+                __syncthreads();
+                // this thread's two digits, from the top down
+                const int lo = EV_BINS - PER * (tid + 1);
+                const int2 c = *reinterpret_cast<const int2 *>(s_hist + lo);
+                const int before = sum_before(c.x + c.y);                         // slots of larger digits
+                if (before < want && before + c.x + c.y >= want) {
+                    const bool first = before + c.y >= want;
+                    s_sel[0] = lo + (first ? 1 : 0);
+                    s_sel[1] = want - before - (first ? 0 : c.y);
+                    s_sel[2] = first ? c.y : c.x;
+                }
+                __syncthreads();
+            } else {
+                // each CTA adds up the cluster's counts of an equal share of the digits and tells
+                // the others their sum; the one whose share the last key's digit lies in tells the digit
+                constexpr int SHARE = EV_BINS / CL;
+                static_assert(SHARE <= EV_THREADS, "a thread has one digit at most");
+                cg::cluster_group cl = cg::this_cluster();
+                cl.sync();
+                const int digit = EV_BINS - 1 - rank * SHARE - tid;               // from the top down
+                int c = 0;
+                if (tid < SHARE) {
+#pragma unroll
+                    for (int r = 0; r < CL; ++r) c += cl.map_shared_rank(s_hist, r)[digit];
+                }
+                int before = sum_before(c);
+                if (tid == SHARE - 1) {
+#pragma unroll
+                    for (int r = 0; r < CL; ++r) cl.map_shared_rank(s_all, r)[rank] = before + c;
+                }
+                cl.sync();
+                for (int r = 0; r < rank; ++r) before += s_all[r];
+                if (tid < SHARE && before < want && before + c >= want) {
+#pragma unroll
+                    for (int r = 0; r < CL; ++r) {
+                        int *sel = cl.map_shared_rank(s_sel, r);
+                        sel[0] = digit;
+                        sel[1] = want - before;
+                        sel[2] = c;
+                    }
+                }
+                cl.sync();
             }
-            if (lane == 31) s_up[warp] = up;
-            __syncthreads();
-            int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s_up[lane] : 0);       // slots of larger digits: the warps' before,
-            before += up - c.x - c.y;                                             // and this one's
-            if (before < want && before + c.x + c.y >= want) {
-                const bool first = before + c.y >= want;
-                s_sel[0] = lo + (first ? 1 : 0);
-                s_sel[1] = want - before - (first ? 0 : c.y);
-                s_sel[2] = first ? c.y : c.x;
-            }
-            __syncthreads();
             prefix = pass == 0 ? (uint32_t)s_sel[0] : (prefix << (above - shift)) | (uint32_t)s_sel[0];
             want = s_sel[1];
             ties = s_sel[2] != want;
@@ -280,8 +329,7 @@ static __global__ void __launch_bounds__(EV_THREADS) kv_evict_kernel(const __gri
     // ---- how many slots each warp keeps, and its place.  Without ties what is
     // kept are the keys from the last one up.
     const uint32_t least = all ? 0u : prefix << shift;
-    const int chunk = (int)(((int64_t)n + EV_THREADS - 1) / EV_THREADS) * 32;     // slots of a warp
-    const int w0 = (int)min((int64_t)n, (int64_t)warp * chunk), w1 = (int)min((int64_t)n, (int64_t)w0 + chunk);
+    const int w0 = (int)min((int64_t)b, a + (int64_t)warp * chunk), w1 = (int)min((int64_t)b, (int64_t)w0 + chunk);
     int n_up = 0, n_eq = 0;
     if (all) {
         n_up = lane == 0 ? w1 - w0 : 0;
@@ -304,6 +352,20 @@ static __global__ void __launch_bounds__(EV_THREADS) kv_evict_kernel(const __gri
     __syncthreads();
     int bu = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s_up[lane] : 0);        // kept, and at the last key, before this warp
     int be = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s_eq[lane] : 0);
+    if constexpr (CL > 1) {
+        cg::cluster_group cl = cg::this_cluster();
+        if (tid == EV_THREADS - 1) {
+            s_cnt[0] = bu + n_up;
+            s_cnt[1] = be + n_eq;
+        }
+        cl.sync();
+        for (int r = 0; r < rank; ++r) {
+            const int *c = cl.map_shared_rank(s_cnt, r);
+            bu += c[0];
+            be += c[1];
+        }
+        cl.sync();                                                                // no CTA leaves while its counts are read
+    }
     // ---- the kept slots in order
     const uint32_t below = (1u << lane) - 1u;
     if (!ties) {
@@ -333,7 +395,13 @@ static __global__ void __launch_bounds__(EV_THREADS) kv_evict_kernel(const __gri
             be += __popc(me);
         }
     }
-    if (h == 0 && tid == 0) p.len_out[s] = m;
+    if (h == 0 && rank == 0 && tid == 0) p.len_out[s] = m;
+}
+
+static __global__ void __launch_bounds__(EV_THREADS) kv_evict_kernel(const __grid_constant__ EvictParams p) { evict_choose<1>(p); }
+static __global__ void __cluster_dims__(EV_CL, 1, 1) __launch_bounds__(EV_THREADS) kv_evict_cluster_kernel(const __grid_constant__ EvictParams p)
+{
+    evict_choose<EV_CL>(p);
 }
 
 // A lane per row of k or v, which goes through shared memory by bulk copies; its

@@ -319,9 +319,12 @@ int kv_evict(const qmv_evict *a, qmv_stream_t stream)
     p.scale_words = c.type == QMV_KV_Q8_0 ? c.head_dim / 64 : 0;
     p.err = di.err;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    static SmemCfg configured_choice, configured;
-    const size_t smem = (size_t)std::min(p.max_len, EV_KEYS) * sizeof(uint32_t);
-    const cudaError_t e = launch_with(kv_evict_kernel, configured_choice, p, dim3((unsigned)c.n_kv_head, (unsigned)a->n_seq), smem, st, false, false, EV_THREADS);
+    static SmemCfg configured_choice[2], configured;
+    const bool many = evict_cluster(p.max_len, a->n_seq * c.n_kv_head, di.sm_count);
+    const dim3 grid((unsigned)(c.n_kv_head * (many ? EV_CL : 1)), (unsigned)a->n_seq);
+    const size_t smem = (size_t)std::min(many ? (int)ceil_div(p.max_len, EV_CL * EV_THREADS) * EV_THREADS : p.max_len, EV_KEYS) * sizeof(uint32_t);
+    const cudaError_t e = many ? launch_with(kv_evict_cluster_kernel, configured_choice[1], p, grid, smem, st, false, false, EV_THREADS)
+                               : launch_with(kv_evict_kernel, configured_choice[0], p, grid, smem, st, false, false, EV_THREADS);
     if (e != cudaSuccess) return finish(e);
     // launched while the choice runs (it waits for its end itself)
     const int per = EV_COPY_THREADS / 32 * EV_SLOTS;

@@ -113,6 +113,19 @@ def test_evict_beyond_the_keys_that_shared_memory_holds(n, budget):
     run_evict("f16", 16, 1, 64, [n], 3, 50, budget, rng.integers(0, 5, (1, 1, n)).astype(np.float32))      # ties
 
 
+def test_evict_long_caches_of_few_and_of_many_heads():
+    """Several CTAs choose for a head where there are few; one does where there are many."""
+    rng = np.random.default_rng(8)
+    lens = [17000, 0, 1, 16384, 8193, 300]
+    for kind, first, last, budget in (("f16", 4, 100, 5000), ("bf16", 0, 0, 1), ("q8", 250, 50, 300)):
+        for score in (rng.standard_normal((6, 2, 17000)), rng.integers(-2, 3, (6, 2, 17000))):
+            run_evict(kind, 64, 2, 64, lens, first, last, budget, score.astype(np.float32), "token")
+    score = rng.standard_normal((1, 20, 41500)).astype(np.float32)
+    score[rng.random(score.shape) < 0.2] = np.nan
+    run_evict("f16", 16, 20, 64, [41500], 1, 1, 41000, score)
+    run_evict("f16", 16, 20, 64, [41500], 1, 1, 900, score)
+
+
 def test_evict_nothing_between_the_ends_and_everything():
     rng = np.random.default_rng(1)
     score = rng.standard_normal((3, 2, 400)).astype(np.float32)
