@@ -14,7 +14,7 @@
 // The best allowed (value, token) goes into the row's 64-bit key as in
 // qmv_argmax; the row's last CTA writes idx_out and zeroes the workspace.
 // Bound by the logits' way in and out: 128 rows of 151937, 2000 of history,
-// 47 us against 24 us of bytes, 35 us of them without history, biases and mask.
+// 46 us against 24 us of bytes, 32 us of them without history, biases and mask.
 // (Slices of 4096 tokens on 256 threads: 45 us, but 8 rows of 128000 with 4096 of
 // history 9.6 instead of 8.8 us; of 16384: 70 us, too few CTAs to overlap their
 // phases.  With the logits loaded into registers chunk by chunk: 54 to 65 us.)

@@ -283,6 +283,9 @@ int kv_evict(const qmv_evict *a, qmv_stream_t stream)
     const int64_t rows = (int64_t)a->n_seq * c.n_kv_head;
     if (overlap(a->score_out, ((rows - 1) * a->score_out_stride + a->budget) * 4, a->score, ((rows - 1) * a->score_stride + std::min(slots, a->score_stride)) * 4) ||
         overlap(a->len_out, (int64_t)a->n_seq * 4, a->kv_len, (int64_t)a->n_seq * 4)) return QMV_ERR_SHAPE;
+    const int per = EV_COPY_THREADS / 32 * EV_SLOTS;                                          // slots of a CTA of the copy
+    const int64_t gx = ceil_div(std::min<int64_t>(a->budget, std::min(slots, a->score_stride)), per) * c.n_kv_head;
+    if (gx > INT_MAX) return QMV_ERR_SHAPE;
     if (host_injected_failure()) return QMV_ERR_CUDA;
     HostDev di;
     if ((rc = host_dev(di))) return rc;
@@ -327,9 +330,6 @@ int kv_evict(const qmv_evict *a, qmv_stream_t stream)
                                : launch_with(kv_evict_kernel, configured_choice[0], p, grid, smem, st, false, false, EV_THREADS);
     if (e != cudaSuccess) return finish(e);
     // launched while the choice runs (it waits for its end itself)
-    const int per = EV_COPY_THREADS / 32 * EV_SLOTS;
-    const int64_t gx = ceil_div(std::min(p.budget, p.max_len), per) * c.n_kv_head;           // at most 2^31 / 64 * 1024 / 16: budget slots fit the table
-    if (gx > INT_MAX) return QMV_ERR_SHAPE;
     return finish(launch_with(kv_evict_copy_kernel, configured, p, dim3((unsigned)gx, (unsigned)a->n_seq), (size_t)per * 2 * p.row_bytes, st, true, false, EV_COPY_THREADS));
 }
 
