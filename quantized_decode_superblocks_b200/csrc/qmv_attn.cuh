@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
     const bool one_page = p.page_size % 16 == 0;                 // 16 slots never leave their page
     constexpr int LPR = G::NCHUNK < 32 ? G::NCHUNK : 32, RPI = 32 / LPR;         // copies: lanes of a slot, slots of a pass
     const int ch = lane % LPR;
-    const int64_t lane_at = (lane / LPR) * p.slot_stride * G::EB + ch * 16, pass_step = RPI * p.slot_stride * G::EB;
+    const uint32_t lane_bytes = ch < nchunk ? 16u : 0u;          // chunks behind the head are zeroed by the copy
+    const int64_t lane_at = (lane / LPR) * p.slot_stride * G::EB + min(ch, nchunk - 1) * 16, pass_step = RPI * p.slot_stride * G::EB;
     const uint32_t k_row = ((lane >> 3) & 1) * 8 + (lane & 7), k_chunk = lane >> 4;       // ldmatrix addresses: K
     const uint32_t v_row = TYPE == KV_Q8_0 ? k_row : (lane >> 4) * 8 + (lane & 7);        // and V
     const uint32_t v_chunk = TYPE == KV_Q8_0 ? k_chunk : (lane >> 3) & 1;
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
                 // rows' addresses: from the first of their 16 where those lie in one page, else from the lane of the row
                 static_assert(RPI <= 16, "a pass's rows lie in one group of 16");
                 const uint32_t to = dst + (uint32_t)(lane / LPR * G::PITCH);
-                if (one_page && use == G::ALL && nchunk == G::NCHUNK) {
+                if (one_page && use == G::ALL) {
 #pragma unroll
                     for (int u = 0; u < SUB; ++u) {
                         const int64_t at = (SUB == 1 ? e : __shfl_sync(0xFFFFFFFFu, e, 16 * u)) * G::EB + lane_at;
@@ -555,8 +556,8 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
 #pragma unroll
                         for (int i = 0; i < 16 / RPI; ++i) {
                             const uint32_t x = to + (uint32_t)((16 * u + i * RPI) * G::PITCH) + ((uint32_t)(ch ^ G::mix(i * RPI + lane / LPR)) << 4);
-                            cp_async16(x, k, 16u);
-                            cp_async16(x + G::KV_BYTES, v, 16u);
+                            cp_async16(x, k, lane_bytes);
+                            cp_async16(x + G::KV_BYTES, v, lane_bytes);
                             k += pass_step;
                             v += pass_step;
                         }
@@ -1212,6 +1213,8 @@ static cudaError_t launch_attn_mb(const AttnParams &p, int sms, int64_t steps, c
 template <int TYPE>
 static cudaError_t launch_attn(const AttnParams &p, int sms, int64_t steps, cudaStream_t st)
 {
+    if constexpr (TYPE != KV_Q8_0)
+        if (p.dim <= 32) return p.mb == 1 ? launch_attn_mb<TYPE, 32, 1>(p, sms, steps, st) : launch_attn_mb<TYPE, 32, 2>(p, sms, steps, st);
     if (p.dim <= 64) return p.mb == 1 ? launch_attn_mb<TYPE, 64, 1>(p, sms, steps, st) : launch_attn_mb<TYPE, 64, 2>(p, sms, steps, st);
     if (p.dim <= 128) return p.mb == 1 ? launch_attn_mb<TYPE, 128, 1>(p, sms, steps, st) : launch_attn_mb<TYPE, 128, 2>(p, sms, steps, st);
     return p.mb == 1 ? launch_attn_mb<TYPE, 256, 1>(p, sms, steps, st) : launch_attn_mb<TYPE, 256, 2>(p, sms, steps, st);
