@@ -1159,7 +1159,8 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
 // score[s][h][j] (+)= sum over the rows of 2^(s_j - m) / l, from the raw scores
 // and the joined (m, l) that attn_decode_kernel left in the workspace.  Two
 // slots a thread, rows in order.  It starts while that kernel ends, and what does
-// not come from it is read before the wait.
+// not come from it is read before the wait.  Plain loads: a slot's rows lie in few
+// lines, which the row by row reads find in L1.
 constexpr int ATT_SCORE_THREADS = 256, ATT_SCORE_SLOTS = 2 * ATT_SCORE_THREADS;
 
 static __global__ void __launch_bounds__(ATT_SCORE_THREADS) attn_score_kernel(const __grid_constant__ AttnParams p)
@@ -1184,10 +1185,10 @@ static __global__ void __launch_bounds__(ATT_SCORE_THREADS) attn_score_kernel(co
         waited = true;
 #pragma unroll 4
         for (int r = 0; r < p.rows; r += 2) {
-            const float4 w = __ldcg(st + r / 2);
+            const float4 w = st[r / 2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float2 u = in[k] ? __ldcg(reinterpret_cast<const float2 *>(p.raw + (sh * p.raw_stride + j[k]) * p.raw_rows + r)) : make_float2(0.f, 0.f);
+                const float2 u = in[k] ? *reinterpret_cast<const float2 *>(p.raw + (sh * p.raw_stride + j[k]) * p.raw_rows + r) : make_float2(0.f, 0.f);
                 given[k] += w.y != 0.f ? ex2(u.x - w.x) * w.y : 0.f;
                 if (r + 1 < p.rows) given[k] += w.w != 0.f ? ex2(u.y - w.z) * w.w : 0.f;
             }
