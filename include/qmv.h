@@ -376,6 +376,7 @@ int kv_append(const qmv_append *a, qmv_stream_t stream);
  *   softmax(s)_j,  f32, entry (s * n_kv_head + h) * score_stride + j;
  * the entries of the newest n_tok slots are set, not added to, so a new slot
  * needs no clearing; entries of slots that no query sees stay as they are.
+ * A length above score_stride is clamped like one beyond the block table.
  * q, out: f32, apart from each other, 16- and 4-byte aligned, token s * n_tok + t at + (s * n_tok + t) *
  * stride floats (q_stride a multiple of 4), heads one after another; n_head a
  * multiple of n_kv_head, 1 <= n_head / n_kv_head * n_tok <= 1024.  The longest

@@ -192,7 +192,9 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     if (e != cudaSuccess || !p.score) return finish(e);
     // launched while the first kernel runs (it waits for its end itself)
     static SmemCfg configured;
-    const unsigned gx = (unsigned)std::min<int64_t>(ceil_div(p.max_len, ATT_SCORE_SLOTS), 1024);
+    // by the longest lengths, but no more than a few waves: the table may be far longer than the sequences
+    const int64_t heads = (int64_t)p.n_kv * p.n_seq;
+    const unsigned gx = (unsigned)std::min<int64_t>(ceil_div(p.max_len, ATT_SCORE_SLOTS), ceil_div(16 * di.sm_count, heads));
     return finish(launch_with(attn_score_kernel, configured, p, dim3(gx, (unsigned)p.n_kv, (unsigned)p.n_seq), 0, st, true, false, ATT_SCORE_THREADS));
 }
 

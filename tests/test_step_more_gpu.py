@@ -105,6 +105,26 @@ def test_attn_scores_captured_and_replayed_on_another_stream(kind):
         assert (np.abs(score.double().cpu().numpy() - want) <= stol).all()
 
 
+def test_attn_lengths_beyond_the_scores_and_tables_far_beyond_the_lengths():
+    rng = np.random.default_rng(14)
+    lens, page, n_kv, dim = [50, 20], 16, 2, 64
+    table, n_pages = make_tables(rng, lens, page)
+    cache = ref.Cache(rng, "f16", n_pages, n_kv, page, dim)
+    x = rng.standard_normal((2, 1, 4 * dim)).astype(np.float32)
+    score = rng.random((2, n_kv, 32)).astype(np.float32)         # room for 32 slots only
+    out, got = run_attn(cache, x, 4, table, lens, 0.125, score=score)
+    assert q.qmv_check() == q.DEVERR_SEQ_LEN
+    want, tol, want_score, stol = ref.attn(cache, x, 4, table, [32, 20], 0.125, score=score)
+    assert (np.abs(out - want) <= tol).all() and (np.abs(got - want_score) <= stol).all()
+    wide = np.full((2, 40000), -1, np.int32)                      # 640000 slots that a later step may reach
+    wide[:, :table.shape[1]] = table
+    score = rng.random((2, n_kv, 640000)).astype(np.float32)
+    out, got = run_attn(cache, x, 4, wide, lens, 0.125, score=score)
+    want, tol, want_score, stol = ref.attn(cache, x, 4, table, lens, 0.125, score=score[:, :, :64])
+    assert (np.abs(out - want) <= tol).all() and (np.abs(got[:, :, :64] - want_score) <= stol).all()
+    assert np.array_equal(got[:, :, 64:].astype(np.float32), score[:, :, 64:])
+
+
 # ------------------------------------------------------------------------------------------------------- eviction --
 @pytest.mark.parametrize("n,budget", [(40959, 1000), (40961, 40000), (50000, 12345)])
 def test_evict_beyond_the_keys_that_shared_memory_holds(n, budget):
