@@ -320,11 +320,12 @@ struct AttnGeom {
     static constexpr int ROWS = 8 * MB;
     static constexpr int NW = attn_warps(TYPE, DP), THREADS = NW * 32;
     // Stages and CTAs a SM: three CTAs with up to 70 KB of shared memory where the
-    // registers allow it (8 narrow rows) or the arithmetic of Q8_0 needs the warps,
+    // registers allow it (narrow heads) or the arithmetic of Q8_0 needs the warps,
     // else two with about 96 KB of ring, one where a stage is 16 KB.  Three against
-    // two: f16, 64 wide, one token over 131071 slots 53.5 -> 51.4 us; Q8_0, 128 wide,
-    // 8 tokens 43.0 -> 41.0 us; f16, 128 wide, 16 rows (two stages left) 46 -> 66 us.
-    static constexpr bool THREE = (MB == 1 && DP <= 64) || (TYPE == KV_Q8_0 && DP == 128);
+    // two: f16, 64 wide, one token over 131071 slots 53.5 -> 51.4 us, 32 rows 20.7 ->
+    // 18.7 us; Q8_0, 128 wide, 8 tokens 43.0 -> 41.0 us; but 64 wide, 16 rows 25 ->
+    // 37 us, and f16, 128 wide, 16 rows (two stages left) 46 -> 66 us.
+    static constexpr bool THREE = (DP <= 64 && (MB == 1 || DP <= 32 || TYPE == KV_F16)) || (TYPE == KV_Q8_0 && DP == 128);
     static constexpr int NST = DP > 128 ? 2 : THREE ? (STAGE >= 8 * 1024 ? 2 : DP == 128 ? 3 : 4) : STAGE >= 8 * 1024 ? 3 : 5;
     static constexpr int RING = NW * NST * STAGE;
     static constexpr int NPQ = TYPE == KV_BF16 ? 3 : 2;          // parts of q
