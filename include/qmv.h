@@ -376,7 +376,9 @@ int kv_append(const qmv_append *a, qmv_stream_t stream);
  *   softmax(s)_j,  f32, entry (s * n_kv_head + h) * score_stride + j;
  * the entries of the newest n_tok slots are set, not added to, so a new slot
  * needs no clearing; entries of slots that no query sees stay as they are.
- * A length above score_stride is clamped like one beyond the block table.
+ * A row of `score` has score_slots entries, 0 standing for score_stride; the
+ * others of its score_stride are not touched (rows of a wider tensor).  A length
+ * above that number is clamped like one beyond the block table.
  * q, out: f32, apart from each other, 16- and 4-byte aligned, token s * n_tok + t at + (s * n_tok + t) *
  * stride floats (q_stride a multiple of 4), heads one after another; n_head a
  * multiple of n_kv_head, 1 <= n_head / n_kv_head * n_tok <= 1024.  The longest
@@ -405,6 +407,7 @@ typedef struct {
     int32_t window, n_sink;
     void *workspace;
     size_t workspace_bytes;
+    int64_t score_slots;        /* <= score_stride; 0: score_stride             */
 } qmv_attn;
 
 int attn_decode(const qmv_attn *a, qmv_stream_t stream);
@@ -426,20 +429,23 @@ size_t attn_ws_bytes(const qmv_kv_cache *cache, int n_head, int n_seq, int n_tok
  *   score_out[s][h][i] = its score                    f32, as score, with score_out_stride
  *   len_out[s]         = min(kv_len[s], budget)       int32 [n_seq]
  * Entries and slots behind the new length are left as they were.  score_out may not
- * overlap score, nor len_out kv_len.  Slots of bad source pages
+ * overlap score, nor len_out kv_len.  A row of `score` has score_slots
+ * entries (0: score_stride of them), and a length above that number is clamped
+ * like one beyond the block table.  Slots of bad source pages
  * take part in the choice but their values are not copied; bad destination
  * pages are not written. */
 typedef struct {
     qmv_kv_cache cache;
     const float *score;
     float *score_out;
-    int64_t score_stride, score_out_stride;     /* >= the slots used            */
+    int64_t score_stride, score_out_stride;     /* >= 1, >= budget              */
     int32_t n_seq, max_pages, dst_max_pages;
     int32_t keep_first, keep_last, budget;      /* keep_first + keep_last <= budget,
                                                    1 <= budget <= dst_max_pages * page_size */
     int64_t table_stride, dst_table_stride;
     const int32_t *block_table, *kv_len, *dst_table;
     int32_t *kept, *len_out;
+    int64_t score_slots;                        /* <= score_stride; 0: score_stride */
 } qmv_evict;
 
 int kv_evict(const qmv_evict *a, qmv_stream_t stream);

@@ -26,6 +26,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // true when a stride of b-element rows can be multiplied by n rows in 64 bits
 bool stride_ok(int64_t v, int64_t least) { return v >= least && v <= (int64_t)1 << 40; }
+// Rows of `score`: their entries (0: as many as the stride) may not reach into the next row.
+bool score_ok(int64_t stride, int64_t slots) { return stride_ok(stride, 1) && slots >= 0 && slots <= stride; }
+int64_t score_width(int64_t stride, int64_t slots) { return slots ? slots : stride; }
 
 int check_cache(const qmv_kv_cache &c)
 {
@@ -131,7 +134,7 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     if ((rc = check_table(c, a->n_seq, a->max_pages, a->table_stride, &slots))) return rc;
     if ((rc = attn_ws(c.type, c.head_dim, c.n_kv_head, a->n_head, a->n_seq, a->n_tok, slots, a->score != nullptr, w))) return rc;
     const int64_t width = (int64_t)a->n_head * c.head_dim;
-    if (!stride_ok(a->q_stride, width) || !stride_ok(a->out_stride, width) || (a->score && !stride_ok(a->score_stride, 1))) return QMV_ERR_SHAPE;
+    if (!stride_ok(a->q_stride, width) || !stride_ok(a->out_stride, width) || (a->score && !score_ok(a->score_stride, a->score_slots))) return QMV_ERR_SHAPE;
     if (a->window < 0 || a->n_sink < 0 || !(a->scale - a->scale == 0.f)) return QMV_ERR_SHAPE;
     if (!aligned(a->q, 16) || a->q_stride % 4 || !aligned(a->out, 4) || !aligned(a->score, 4) || !aligned(a->block_table, 4) ||
         !aligned(a->kv_len, 4) || !aligned(a->workspace, 256)) return QMV_ERR_ALIGN;
@@ -168,7 +171,7 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     p.dim = c.head_dim;
     p.page_size = c.page_size;
     p.page_shift = page_shift(c.page_size);
-    p.max_len = (int)(a->score ? std::min(slots, a->score_stride) : slots);
+    p.max_len = (int)(a->score ? std::min(slots, score_width(a->score_stride, a->score_slots)) : slots);
     p.mb = attn_mb(p.rows);
     p.n_rb = (int)ceil_div(p.rows, 8 * p.mb);
     p.window = a->window >= slots ? 0 : a->window;      // every slot is within a window that long
@@ -278,15 +281,16 @@ int kv_evict(const qmv_evict *a, qmv_stream_t stream)
     if ((rc = check_table(c, a->n_seq, a->dst_max_pages, a->dst_table_stride, &dst_slots))) return rc;
     if (a->keep_first < 0 || a->keep_last < 0 || a->budget < 1 || (int64_t)a->keep_first + a->keep_last > a->budget ||
         a->budget > dst_slots) return QMV_ERR_SHAPE;
-    if (!stride_ok(a->score_stride, 1) || !stride_ok(a->score_out_stride, a->budget)) return QMV_ERR_SHAPE;
+    if (!score_ok(a->score_stride, a->score_slots) || !stride_ok(a->score_out_stride, a->budget)) return QMV_ERR_SHAPE;
+    const int64_t max_len = std::min(slots, score_width(a->score_stride, a->score_slots));
     for (const void *x : {(const void *)a->score, (const void *)a->score_out, (const void *)a->block_table, (const void *)a->kv_len,
                           (const void *)a->dst_table, (const void *)a->kept, (const void *)a->len_out})
         if (!aligned(x, 4)) return QMV_ERR_ALIGN;
     const int64_t rows = (int64_t)a->n_seq * c.n_kv_head;
-    if (overlap(a->score_out, ((rows - 1) * a->score_out_stride + a->budget) * 4, a->score, ((rows - 1) * a->score_stride + std::min(slots, a->score_stride)) * 4) ||
+    if (overlap(a->score_out, ((rows - 1) * a->score_out_stride + a->budget) * 4, a->score, ((rows - 1) * a->score_stride + max_len) * 4) ||
         overlap(a->len_out, (int64_t)a->n_seq * 4, a->kv_len, (int64_t)a->n_seq * 4)) return QMV_ERR_SHAPE;
     const int per = EV_COPY_THREADS / 32 * EV_SLOTS;                                          // slots of a CTA of the copy
-    const int64_t gx = ceil_div(std::min<int64_t>(a->budget, std::min(slots, a->score_stride)), per) * c.n_kv_head;
+    const int64_t gx = ceil_div(std::min<int64_t>(a->budget, max_len), per) * c.n_kv_head;
     if (gx > INT_MAX) return QMV_ERR_SHAPE;
     if (host_injected_failure()) return QMV_ERR_CUDA;
     HostDev di;
@@ -315,7 +319,7 @@ int kv_evict(const qmv_evict *a, qmv_stream_t stream)
     p.n_kv = c.n_kv_head;
     p.page_size = c.page_size;
     p.page_shift = page_shift(c.page_size);
-    p.max_len = (int)std::min(slots, a->score_stride);
+    p.max_len = (int)max_len;
     p.keep_first = a->keep_first;
     p.keep_last = a->keep_last;
     p.budget = a->budget;

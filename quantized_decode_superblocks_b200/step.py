@@ -68,6 +68,8 @@ def _lines(t):
 def _heads(name, t):
     """Stride between the (sequence, head) rows of a [n_seq, n_kv_head, n] tensor."""
     s, h, n = t.shape
+    if n < 1:
+        _fail(f"{name}: needs an entry a row, got {tuple(t.shape)}")
     stride = t.stride(1) if h > 1 else t.stride(0)
     if s > 1 and h > 1 and t.stride(0) != h * t.stride(1):
         _fail(f"{name}: rows must be evenly spaced, got strides {t.stride()}")
@@ -167,7 +169,7 @@ class AttnArgs(_Args):
     _fields_ = [("cache", KvCache), ("q", _vp), ("out", _vp), ("score", _vp), ("q_stride", _i64), ("out_stride", _i64),
                 ("score_stride", _i64), ("n_head", _i32), ("n_seq", _i32), ("n_tok", _i32), ("max_pages", _i32),
                 ("table_stride", _i64), ("block_table", _vp), ("kv_len", _vp), ("scale", _f32), ("window", _i32),
-                ("n_sink", _i32), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+                ("n_sink", _i32), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("score_slots", _i64)]
 
     def __init__(self, cache, q, out, block_table, kv_len, workspace, scale, window=0, n_sink=0, score=None):
         super().__init__()
@@ -184,7 +186,7 @@ class AttnArgs(_Args):
         self.max_pages, self.table_stride = self._tables(block_table, kv_len)
         if score is not None:
             _take(self, "score", score, "float32", 3, (self.n_seq, cache.n_kv_head, None))
-            self.score_stride = _heads("score", score)
+            self.score_stride, self.score_slots = _heads("score", score), score.shape[2]
         self.scale, self.window, self.n_sink = scale, window, n_sink
         _take(self, "workspace", workspace, "uint8", 1)
         self.workspace_bytes = workspace.numel()
@@ -198,7 +200,7 @@ class EvictArgs(_Args):
                 ("score_out_stride", _i64), ("n_seq", _i32), ("max_pages", _i32), ("dst_max_pages", _i32),
                 ("keep_first", _i32), ("keep_last", _i32), ("budget", _i32), ("table_stride", _i64),
                 ("dst_table_stride", _i64), ("block_table", _vp), ("kv_len", _vp), ("dst_table", _vp), ("kept", _vp),
-                ("len_out", _vp)]
+                ("len_out", _vp), ("score_slots", _i64)]
 
     def __init__(self, cache, score, block_table, kv_len, dst_table, kept, score_out, len_out, keep_first, keep_last,
                  budget):
@@ -211,6 +213,7 @@ class EvictArgs(_Args):
         if score_out.shape[2] < budget:
             _fail(f"score_out: {score_out.shape[2]} entries a head, the budget is {budget}")
         self.score_stride, self.score_out_stride = _heads("score", score), _heads("score_out", score_out)
+        self.score_slots = score.shape[2]
         _take(self, "kept", kept, "int32", 3, (self.n_seq, cache.n_kv_head, budget))
         if not kept.is_contiguous():
             _fail("kept: must be contiguous")

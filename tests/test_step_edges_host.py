@@ -1,0 +1,76 @@
+"""Calls at the edges of what the cache and logits operators take, as far as they show without a GPU: what an
+argument object lets a call touch, and which mistakes the tests' bounds tell apart."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import quantized_decode_superblocks_b200 as q
+from test_step_host import A, SHAPE, L, attn, evict, good  # noqa: F401
+
+
+class Fake:
+    """A CPU tensor that says it lies on cuda:0: for argument objects that no call gets."""
+
+    def __init__(self, t):
+        self.t, self.device, self.dtype, self.shape = t, torch.device("cuda", 0), t.dtype, t.shape
+
+    def dim(self):
+        return self.t.dim()
+
+    def stride(self, *i):
+        return self.t.stride(*i)
+
+    def data_ptr(self):
+        return self.t.data_ptr()
+
+    def numel(self):
+        return self.t.numel()
+
+    def is_contiguous(self):
+        return self.t.is_contiguous()
+
+
+def zeros(*shape, dtype=torch.float32):
+    return Fake(torch.zeros(*shape, dtype=dtype))
+
+
+def small_cache():
+    return q.KvCache(q.KV_F16, zeros(80, 2, 16, 64, dtype=torch.float16), zeros(80, 2, 16, 64, dtype=torch.float16))
+
+
+def attn_args(score):
+    return q.AttnArgs(small_cache(), zeros(2, 1, 512), zeros(2, 1, 512), zeros(2, 40, dtype=torch.int32), zeros(2, dtype=torch.int32),
+                      zeros(1 << 22, dtype=torch.uint8), 0.125, score=score)
+
+
+def evict_args(score):
+    return q.EvictArgs(small_cache(), score, zeros(2, 40, dtype=torch.int32), zeros(2, dtype=torch.int32), zeros(2, 2, dtype=torch.int32),
+                       zeros(2, 2, 32, dtype=torch.int32), zeros(2, 2, 32), zeros(2, dtype=torch.int32), 4, 8, 32)
+
+
+@pytest.mark.parametrize("make", [attn_args, evict_args])
+@pytest.mark.parametrize("lo,hi", [(0, 1000), (900, 1000), (0, 100), (999, 1000)])
+def test_rows_of_a_wider_score_end_where_the_tensor_ends(make, lo, hi):
+    """640 slots a sequence: whatever the lengths are, no entry behind a row's last one is reached."""
+    whole = torch.zeros(2, 2, 1000)
+    args = make(Fake(whole[:, :, lo:hi]))
+    reach = min(640, getattr(args, "score_slots", 0) or args.score_stride)
+    assert args.score_stride == 1000 and reach == min(640, hi - lo)
+    assert args.score + (3 * 1000 + reach) * 4 <= whole.data_ptr() + whole.numel() * 4
+
+
+@pytest.mark.parametrize("make", [attn_args, evict_args])
+def test_a_score_without_entries_is_refused(make):
+    with pytest.raises(ValueError, match="entry a row"):
+        make(Fake(torch.zeros(2, 2, 0)))
+
+
+def test_score_rows_may_not_reach_into_each_other(L):  # noqa: F811
+    for call, kw in ((attn, dict(score=A)), (evict, {})):
+        assert good(L, call, score_stride=64, score_slots=64, **kw) and good(L, call, score_stride=64, score_slots=1, **kw)
+        assert good(L, call, score_stride=64, score_slots=0, **kw)
+        assert call(L, score_stride=64, score_slots=65, **kw) == SHAPE and call(L, score_stride=64, score_slots=-1, **kw) == SHAPE
+    # outputs may lie between the rows' entries' end and the buffer's
+    end = A + (15 * 64 + 20) * 4
+    assert evict(L, score_slots=20, score_out=end - 4) == SHAPE and good(L, evict, score_slots=20, score_out=end)
