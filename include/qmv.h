@@ -304,7 +304,8 @@ int qmv_argmax(int fmt, const void *W_blocks, int64_t rows, int64_t cols,
  * left out (not read, not written, not attended) and QMV_DEVERR_PAGE_ID is
  * recorded.  Entries whose slots a call does not touch are never read as pages
  * (pages behind a sliding window may have been freed).  A length below 0 or above
- * max_pages * page_size is clamped and QMV_DEVERR_SEQ_LEN recorded.
+ * max_pages * page_size records QMV_DEVERR_SEQ_LEN; attn_decode and kv_evict
+ * clamp it, kv_append leaves the tokens out whose slots lie outside.
  * Sequences may share pages that no call writes.
  */
 typedef enum { QMV_KV_F16 = 0, QMV_KV_BF16 = 1, QMV_KV_Q8_0 = 2 } qmv_kv_type;
@@ -335,7 +336,8 @@ typedef struct {
  * Token t (0 <= t < n_tok) of sequence s goes to slot kv_len[s] - n_tok + t
  * (kv_len counts the new tokens already) at position pos[s * n_tok + t], or at
  * its slot number where pos is NULL.  A token whose slot is negative (a padded
- * batch) or whose page is bad is not stored; its rotated q is written all the same.
+ * batch) or lies beyond the block table, or whose page is bad, is not stored; its
+ * rotated q is written all the same.
  * q, k, v: f32, token s * n_tok + t at + (s * n_tok + t) * stride floats, its heads
  * one after another: rows of a fused QKV product are read as they lie (q = y,
  * k = y + n_head * head_dim, all three strides the row length).  q_out: f32,

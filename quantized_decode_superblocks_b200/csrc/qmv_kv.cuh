@@ -61,15 +61,16 @@ static __global__ void __launch_bounds__(APP_THREADS, APP_CTAS) kv_append_kernel
     __shared__ long long s_at;                     // the slot's first element, -1: nothing to store
     const int t = blockIdx.x, s = blockIdx.y, tok = s * p.n_tok + t;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int raw = __ldg(p.kv_len + s), len = min(max(raw, 0), p.max_len), slot = len - p.n_tok + t;
+    const int raw = __ldg(p.kv_len + s);
+    const long long slot = (long long)raw - p.n_tok + t;     // of the length as given: a clamped one would move the tokens onto slots in use
     if (threadIdx.x == 0) {
         long long at = -1;
-        if (slot >= 0) {
-            const int i = page_of(slot, p), page = __ldg(p.table + (int64_t)s * p.table_stride + i);
-            if (page >= 0 && page < p.n_pages) at = page * p.page_stride + (slot - i * p.page_size) * p.slot_stride;
+        if (slot >= 0 && slot < p.max_len) {
+            const int j = (int)slot, i = page_of(j, p), page = __ldg(p.table + (int64_t)s * p.table_stride + i);
+            if (page >= 0 && page < p.n_pages) at = page * p.page_stride + (j - i * p.page_size) * p.slot_stride;
             else atomicOr(p.err, 8 /* QMV_DEVERR_PAGE_ID */);
         }
-        if (raw != len) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
+        if (raw < 0 || raw > p.max_len) atomicOr(p.err, 16 /* QMV_DEVERR_SEQ_LEN */);
         s_at = at;
     }
     const int nq = p.q_out ? p.n_head : 0, heads = nq + 2 * p.n_kv;
@@ -95,7 +96,7 @@ static __global__ void __launch_bounds__(APP_THREADS, APP_CTAS) kv_append_kernel
         }
     };
     load();
-    const double pos = p.pos ? __ldg(p.pos + tok) : slot;
+    const double pos = p.pos ? (double)__ldg(p.pos + tok) : (double)slot;
     for (int i = threadIdx.x; i < half; i += APP_THREADS) s_turn[i] = rope_turn(pos, __ldg(p.inv_freq + i));
     __syncthreads();
     const long long at = s_at;

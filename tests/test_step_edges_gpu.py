@@ -58,3 +58,52 @@ def test_scores_in_a_slice_of_a_wider_tensor():
         for h in range(n_kv):
             assert kept[s, h].tolist() == rows[s][h] and np.array_equal(so[s, h].cpu().numpy(), z[s, h, rows[s][h]])
     assert n_out.tolist() == [budget, budget]
+
+
+# ------------------------------------------------------------------------------------------ append: what is stored --
+def pools(cache, k, v, ks, vs):
+    """What the pools hold now, bit by bit: the quants (16-bit values as integers), and the scales."""
+    return [x.contiguous().view(torch.int16 if x.dtype != torch.int8 else torch.int8).cpu().numpy() for x in (k, v, ks, vs) if x is not None]
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "q8"])
+@pytest.mark.parametrize("own_positions", [False, True])
+def test_append_tokens_beyond_the_table_are_not_stored(kind, own_positions):
+    """Every token goes to its own slot or nowhere: nothing is moved back over slots that are in use."""
+    rng = np.random.default_rng(3)
+    page, n_kv, n_head, dim, n_tok = 16, 2, 4, 64, 3
+    lens = [32, 33, 34, 35, 36, 1000, 2 ** 31 - 1, 2, 0, -1, -2 ** 31]
+    table = np.arange(2 * len(lens), dtype=np.int32).reshape(-1, 2)
+    cache = ref.Cache(rng, kind, table.size, n_kv, page, dim)
+    k, v, ks, vs = cache.device()
+    before = pools(cache, k, v, ks, vs)
+    x = rng.standard_normal((len(lens), n_tok, (n_head + 2 * n_kv) * dim)).astype(np.float32)
+    inv = (10000.0 ** (-2.0 * np.arange(dim // 2) / dim)).astype(np.float32)
+    qd, kd, vd = dev(x).split([n_head * dim, n_kv * dim, n_kv * dim], -1)
+    out = torch.zeros(len(lens), n_tok, n_head * dim, device="cuda")
+    pos = rng.integers(0, 5000, (len(lens), n_tok)).astype(np.int32)
+    q.kv_append(q.AppendArgs(q.KvCache(base.KINDS[kind], k, v, ks, vs), qd, kd, vd, out, dev(table), dev(np.array(lens, np.int32)),
+                             pos=dev(pos) if own_positions else None, inv_freq=dev(inv), rope_dim=dim))
+    assert q.qmv_check() == q.DEVERR_SEQ_LEN
+    after = pools(cache, k, v, ks, vs)
+    got = out.double().cpu().numpy().reshape(len(lens), n_tok, n_head, dim)
+    stored = {(s, n - n_tok + t) for s, n in enumerate(lens) for t in range(n_tok) if 0 <= n - n_tok + t < 32}
+    for s, n in enumerate(lens):
+        for t in range(n_tok):
+            at = int(pos[s, t]) if own_positions else n - n_tok + t
+            want = ref.rope(x[s, t, :n_head * dim].reshape(n_head, dim), float(at), inv, dim, False)
+            assert (np.abs(got[s, t] - want) <= 2 * ref.U * np.abs(want) + 1e-12 * np.abs(x[s, t]).max()).all(), (n, t)
+        for j in range(32):
+            same = all(np.array_equal(a[2 * s + j // 16, :, j % 16], b[2 * s + j // 16, :, j % 16]) for a, b in zip(after, before))
+            assert same == ((s, j) not in stored), (n, j)
+    new = [(s, t) for s, n in enumerate(lens) for t in range(n_tok) if (s, n - n_tok + t) in stored]
+    for s, t in new:                                    # the values are those of the token itself
+        j = lens[s] - n_tok + t
+        y = v[2 * s + j // 16, :, j % 16].double()
+        if kind == "q8":
+            y = (y.reshape(n_kv, -1, 32) * vs[2 * s + j // 16, :, j % 16].double()[..., None]).reshape(n_kv, dim)
+        want = x[s, t, -n_kv * dim:].reshape(n_kv, dim).astype(np.float64)
+        half = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}.get(kind)
+        # Q8_0: half a step of a block of 32, whose scale is rounded to f16
+        lim = np.abs(want) * half + 2.0 ** -25 if half else np.repeat(np.abs(want.reshape(n_kv, -1, 32)).max(-1) / 127 * (0.5 + 127 * 2.0 ** -11 + 1e-3), 32, -1)
+        assert (np.abs(y.cpu().numpy() - want) <= lim).all()
