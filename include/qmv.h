@@ -332,7 +332,11 @@ typedef struct {
  *   positions keep their phase; the sums with 48 bits of either, rounded once
  *   to f32, then to the cache's type)
  *   Q8_0 blocks: scale = f16(min(amax / 127, 65504)), quant = value / scale
- *   rounded to even and clamped to +-127, 0 where the scale is 0.
+ *   rounded to even and clamped to +-127, 0 where the scale is 0; a block
+ *   with a NaN gets the scale NaN and quants 0, an infinity counts as the
+ *   largest value that the block can hold
+ *   f16: values beyond its range become infinities, and NaN stays NaN in it
+ *   and in bf16; attn_decode does not take either in a slot that it sees
  * Token t (0 <= t < n_tok) of sequence s goes to slot kv_len[s] - n_tok + t
  * (kv_len counts the new tokens already) at position pos[s * n_tok + t], or at
  * its slot number where pos is NULL.  A token whose slot is negative (a padded

@@ -142,7 +142,9 @@ static __global__ void __launch_bounds__(APP_THREADS, APP_CTAS) kv_append_kernel
                 const float w = y[b];
                 float mx = fabsf(w);
                 for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-                const __half dh = __float2half_rn(fminf(__fdiv_rn(mx, 127.f), 65504.f));
+                // a NaN, which the maximum passes over, makes the scale one: the block reads as NaN
+                const bool bad = __any_sync(0xFFFFFFFFu, w != w);
+                const __half dh = __float2half_rn(bad ? __int_as_float(0x7FFFFFFF) : fminf(__fdiv_rn(mx, 127.f), 65504.f));
                 const float df = __half2float(dh);
                 const float qv = df > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(w, df)), -127.f), 127.f) : 0.f;
                 reinterpret_cast<int8_t *>(pool)[e] = (int8_t)(int)qv;

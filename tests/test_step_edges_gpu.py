@@ -107,3 +107,32 @@ def test_append_tokens_beyond_the_table_are_not_stored(kind, own_positions):
         # Q8_0: half a step of a block of 32, whose scale is rounded to f16
         lim = np.abs(want) * half + 2.0 ** -25 if half else np.repeat(np.abs(want.reshape(n_kv, -1, 32)).max(-1) / 127 * (0.5 + 127 * 2.0 ** -11 + 1e-3), 32, -1)
         assert (np.abs(y.cpu().numpy() - want) <= lim).all()
+
+
+@pytest.mark.parametrize("what", [float("nan"), -float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dim", [64, 192, 256])
+def test_append_keeps_nan_in_a_q8_cache(what, dim):
+    """A block of 32 with a NaN reads as NaN throughout, one with an infinity at its largest scale; other blocks as ever."""
+    rng = np.random.default_rng(dim)
+    n_kv, page = 2, 16
+    cache = ref.Cache(rng, "q8", 1, n_kv, page, dim)
+    k, v, ks, vs = cache.device()
+    x = rng.standard_normal((1, 1, 2 * n_kv * dim)).astype(np.float32)
+    spots = [3, dim + 40, n_kv * dim + 63, 2 * n_kv * dim - 1]              # of k and of v, in either head
+    x[0, 0, spots] = what
+    kd, vd = dev(x).split([n_kv * dim, n_kv * dim], -1)
+    q.kv_append(q.AppendArgs(q.KvCache(q.KV_Q8_0, k, v, ks, vs), None, kd, vd, None, dev(np.zeros((1, 1), np.int32)), dev(np.array([7], np.int32))))
+    b = x.reshape(2, n_kv, dim // 32, 32)
+    f = np.float32
+    with np.errstate(invalid="ignore"):
+        d = np.minimum(np.abs(b).max(-1) / f(127), f(65504)).astype(np.float16)
+        df = d.astype(np.float32)[..., None]
+        quant = np.clip(np.rint(b / df), -127, 127)
+    quant = np.where(np.isnan(df), 0, quant).astype(np.int8)
+    spoiled = 0
+    for i, (pool, scale) in enumerate(((k, ks), (v, vs))):
+        got_q = pool[0, :, 6].cpu().numpy().reshape(n_kv, -1, 32)
+        got_d = scale[0, :, 6].cpu().numpy()
+        assert np.array_equal(got_d, d[i], equal_nan=True) and np.array_equal(got_q, quant[i])
+        spoiled += np.isnan(got_d).sum()
+    assert spoiled == (4 if np.isnan(what) else 0)
