@@ -30,12 +30,13 @@ __device__ __forceinline__ float4 rope_turn(double pos, float f)
     return make_float4(ch, (float)(c - ch), sh, (float)(sn - sh));
 }
 
-// a c + b s, rounded once: the products' and the sum's roundings are caught in f32.
+// a c + b s, rounded once: the products' and the sum's roundings are caught in f32.  Infinities, also those of
+// a sum beyond f32's range, and NaN are final: what they leave would be infinity minus infinity.
 __device__ __forceinline__ float rope_sum(float a, float b, float4 t)
 {
     const float p = a * t.x, q = b * t.z, r = p + q, v = r - p;
     const float left = fmaf(a, t.y, fmaf(a, t.x, -p)) + fmaf(b, t.w, fmaf(b, t.z, -q));
-    return r + (((p - (r - v)) + (q - v)) + left);
+    return fabsf(r) < INFINITY ? r + (((p - (r - v)) + (q - v)) + left) : r;
 }
 
 struct AppendParams {

@@ -136,3 +136,40 @@ def test_append_keeps_nan_in_a_q8_cache(what, dim):
         assert np.array_equal(got_d, d[i], equal_nan=True) and np.array_equal(got_q, quant[i])
         spoiled += np.isnan(got_d).sum()
     assert spoiled == (4 if np.isnan(what) else 0)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("style", [q.ROPE_HALVES, q.ROPE_PAIRS])
+def test_append_infinities_turn_as_the_formula_says(kind, style):
+    """a cos - b sin with an infinity, with two, with a NaN, and with values whose sum passes f32's range."""
+    dim, page, pos = 64, 16, [0, 1, 700, 31]
+    inf, big = np.inf, np.float32(3e38)
+    x = np.ones((len(pos), 1, 3 * dim), np.float32)
+    for s in range(len(pos)):
+        for i, (a, b) in enumerate([(inf, 1), (1, inf), (-inf, 2), (inf, inf), (inf, -inf), (np.nan, 1), (1, np.nan), (big, big), (big, -big), (-big, -big), (0, inf)]):
+            at = (2 * i, 2 * i + 1) if style == q.ROPE_PAIRS else (i, i + dim // 2)
+            for h in range(2):                          # q and k
+                x[s, 0, h * dim + at[0]], x[s, 0, h * dim + at[1]] = a, b
+    inv = np.full(dim // 2, 0.7, np.float32)
+    cache = ref.Cache(np.random.default_rng(0), kind, len(pos), 1, page, dim)
+    k, v, _, _ = cache.device()
+    qd, kd, vd = dev(x).split([dim, dim, dim], -1)
+    out = torch.zeros(len(pos), 1, dim, device="cuda")
+    q.kv_append(q.AppendArgs(q.KvCache(base.KINDS[kind], k, v), qd, kd, vd, out, dev(np.arange(len(pos), dtype=np.int32)[:, None]),
+                             dev(np.ones(len(pos), np.int32)), pos=dev(np.array(pos, np.int32)[:, None]), inv_freq=dev(inv), rope_dim=dim, rope_style=style))
+    half = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}[kind]
+    with np.errstate(invalid="ignore", over="ignore"):
+        for s, at in enumerate(pos):
+            want = ref.rope(x[s, 0, :dim], at, inv, dim, style == q.ROPE_PAIRS).astype(np.float32).astype(np.float64)
+            got = out[s, 0].double().cpu().numpy()
+            ok = np.isfinite(want)
+            assert np.array_equal(got[~ok], want[~ok], equal_nan=True), (at, got, want)
+            assert (np.abs(got[ok] - want[ok]) <= 2 * ref.U * np.abs(want[ok]) + 1e-12).all()
+            kept = k[s, 0, 0].double().cpu().numpy()
+            if kind == "f16":                           # what is beyond 65504 is an infinity there
+                want = want.astype(np.float16).astype(np.float64)
+                ok = np.isfinite(want)
+            else:
+                ok = np.abs(want) < 3.38e38
+            assert np.array_equal(np.isnan(kept), np.isnan(want)) and np.array_equal(np.sign(kept[~np.isnan(kept)]), np.sign(want[~np.isnan(want)]))
+            assert np.isinf(kept[np.isinf(want)]).all() and (np.abs(kept[ok] - want[ok]) <= 2 * half * np.abs(want[ok]) + 2.0 ** -24).all()
