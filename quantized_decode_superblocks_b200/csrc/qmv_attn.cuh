@@ -29,8 +29,11 @@
 //   f16 cache:   q * 2^e (per row, so that the largest value is below 2^13) and
 //                2^9 * p as two f16 parts: 22 bits;
 //   bf16 cache:  q and p as three bf16 parts, 24 bits;
-//   Q8_0 cache:  as for f16 (int8 is exact in it), with p * scale over a power
-//                of two for every 16 slots and 32 dims in the place of p.
+//   Q8_0 cache:  q as for f16 (int8 is exact in it), and p * scale as two f16
+//                parts times a power of two of its own for every row, tile and
+//                block of 32 dims, since scales may lie 2^40 apart.  (As three bf16
+//                parts without a factor, which int8 is exact in too: one token for
+//                16 sequences, 128 wide, 98 us instead of 84, 64 wide 56 instead of 50.)
 // Tensor cores cut off the bits that an accumulation shifts out, so a long chain of
 // them drifts: each tile's product starts from zero and is added to the
 // running output by rounded f32 adds.
@@ -74,7 +77,7 @@ constexpr int ATT_MIN_TILE = 16, ATT_MAX_TILE = 32;
 // parts: together below 2^16, and the second keeps what an f16 part cuts off
 // (half a step of its subnormals) below 2^-34 of the reference.  bf16 parts
 // have f32's range.
-__host__ __device__ constexpr float attn_slack(int type) { return type == 1 ? 12.f : 6.f; }
+__host__ __device__ constexpr float attn_slack(int type) { return type == 0 ? 6.f : 12.f; }
 constexpr float ATT_F16_SHIFT = 9.f;
 
 // 8-row blocks that one CTA takes: up to 2.  (With 4, whose outputs and operands
@@ -274,7 +277,7 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t x)
         return *reinterpret_cast<const uint32_t *>(&y);
     }
 }
-// (a, b) += (x, y), *= (x, y), += (x, y) * f: one instruction each.
+// (a, b) += (x, y), += (x, y) * f, += (x f, y g), *= (x, y): one instruction each.
 __device__ __forceinline__ void add2(float &a, float &b, float x, float y)
 {
     asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
@@ -284,6 +287,11 @@ __device__ __forceinline__ void fma2(float &a, float &b, float x, float y, float
 {
     asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %4};\n\tfma.rn.f32x2 u, v, w, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
         : "+f"(a), "+f"(b) : "f"(x), "f"(y), "f"(f));
+}
+__device__ __forceinline__ void fma22(float &a, float &b, float x, float y, float f, float g)
+{
+    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %5};\n\tfma.rn.f32x2 u, v, w, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y), "f"(f), "f"(g));
 }
 __device__ __forceinline__ void mul2(float &a, float &b, float x, float y)
 {
@@ -887,34 +895,18 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
 #pragma unroll
                 for (int b = 0; b < DP / 32; ++b) {
                     const uint32_t sa = buf + 2 * G::KV_BYTES + G::SC_BYTES + 2 * b;
-                    float d[SUB][4], dm = 0.f;
+                    float d[SUB][4];
 #pragma unroll
                     for (int u = 0; u < SUB; ++u)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             d[u][i] = half_bits_to_float(lds_u16(sa + (16 * u + 2 * c4 + (i & 1) + (i >> 1) * 8) * G::SC_PITCH));
-                            dm = fmaxf(dm, fabsf(d[u][i]));
+                            // NaN or infinity of a slot that a row may not see: its weight is 0
+                            if (mixed && !(fabsf(d[u][i]) < INFINITY)) d[u][i] = 0.f;
                         }
-                    if (mixed) {                                          // NaN or infinity of a slot that a row may not see: its weight is 0
-                        dm = 0.f;
-#pragma unroll
-                        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (!(fabsf(d[u][i]) < INFINITY)) d[u][i] = 0.f;
-                                dm = fmaxf(dm, fabsf(d[u][i]));
-                            }
-                    }
-                    // the scales over a power of two at least the largest of them: their products with the weights stay in f16
-                    dm = fmaxf(dm, __shfl_xor_sync(0xFFFFFFFFu, dm, 1));
-                    dm = fmaxf(dm, __shfl_xor_sync(0xFFFFFFFFu, dm, 2));
-                    const uint32_t ex = min(__float_as_uint(dm) >> 23, 200u);
-                    const float down = __uint_as_float((253u - ex) << 23), back = __uint_as_float((ex + 1u) << 23);
                     uint32_t a[SUB][2][4];
 #pragma unroll
                     for (int u = 0; u < SUB; ++u) {
-                        mul2(d[u][0], d[u][1], down, down);
-                        mul2(d[u][2], d[u][3], down, down);
                         uint32_t r[4];
                         ldsm4t(r, va + G::at(16 * u + v_row, 2 * b + v_chunk));
 #pragma unroll
@@ -926,13 +918,29 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
 #pragma unroll
                     for (int nb = 0; nb < MB; ++nb) {
                         uint32_t pb[SUB][2][2];
+                        float pd[SUB][4], top = 0.f;
 #pragma unroll
                         for (int u = 0; u < SUB; ++u) {
-                            float pd[4] = {pw[nb][u][0], pw[nb][u][1], pw[nb][u][2], pw[nb][u][3]};
-                            mul2(pd[0], pd[1], d[u][0], d[u][1]);
-                            mul2(pd[2], pd[3], d[u][2], d[u][3]);
-                            split_f16(pd[0], pd[1], pb[u][0][0], pb[u][1][0]);
-                            split_f16(pd[2], pd[3], pb[u][0][1], pb[u][1][1]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) pd[u][i] = pw[nb][u][i];
+                            mul2(pd[u][0], pd[u][1], d[u][0], d[u][1]);
+                            mul2(pd[u][2], pd[u][3], d[u][2], d[u][3]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(pd[u][i]));
+                        }
+                        // the row's products times the power of two that brings the largest below 2^15: what the parts
+                        // leave of the others is at most 2^-39 of it, whatever the scales of slots without weight are
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                        const uint32_t ex = max(__float_as_uint(top) & 0x7F800000u, 15u << 23);
+                        const float down = __uint_as_float((268u << 23) - ex), own = __uint_as_float(ex - (14u << 23));
+                        const float back0 = __shfl_sync(0xFFFFFFFFu, own, 8 * c4), back1 = __shfl_sync(0xFFFFFFFFu, own, 8 * c4 + 4);
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) {
+                            mul2(pd[u][0], pd[u][1], down, down);
+                            mul2(pd[u][2], pd[u][3], down, down);
+                            split_f16(pd[u][0], pd[u][1], pb[u][0][0], pb[u][1][0]);
+                            split_f16(pd[u][2], pd[u][3], pb[u][0][1], pb[u][1][1]);
                         }
 #pragma unroll
                         for (int k2 = 0; k2 < 2; ++k2) {
@@ -942,8 +950,8 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
                             for (int u = 1; u < SUB; ++u) mma_16<false>(t, a[u][k2], pb[u][1][0], pb[u][1][1]);
 #pragma unroll
                             for (int u = 0; u < SUB; ++u) mma_16<false>(t, a[u][k2], pb[u][0][0], pb[u][0][1]);
-                            fma2(acc[nb][2 * b + k2][0], acc[nb][2 * b + k2][1], t[0], t[1], back);
-                            fma2(acc[nb][2 * b + k2][2], acc[nb][2 * b + k2][3], t[2], t[3], back);
+                            fma22(acc[nb][2 * b + k2][0], acc[nb][2 * b + k2][1], t[0], t[1], back0, back1);
+                            fma22(acc[nb][2 * b + k2][2], acc[nb][2 * b + k2][3], t[2], t[3], back0, back1);
                         }
                     }
                 }

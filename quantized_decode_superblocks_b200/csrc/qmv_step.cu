@@ -177,7 +177,7 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     p.window = a->window >= slots ? 0 : a->window;      // every slot is within a window that long
     p.n_sink = a->n_sink;
     p.scale_log2 = a->scale * 1.4426950408889634f;
-    p.l_shift = c.type == QMV_KV_BF16 ? 0.f : ATT_F16_SHIFT;
+    p.l_shift = c.type == QMV_KV_F16 ? ATT_F16_SHIFT : 0.f;
     uint8_t *ws = static_cast<uint8_t *>(a->workspace);
     p.counters = reinterpret_cast<unsigned *>(ws);
     p.part_ml = reinterpret_cast<float *>(ws + w.ml);

@@ -8,6 +8,7 @@ import torch
 
 import quantized_decode_superblocks_b200 as q
 import step_ref as ref
+import step_tight as tight
 import test_step_gpu as base
 from test_step_gpu import dev, make_tables
 
@@ -173,3 +174,66 @@ def test_append_infinities_turn_as_the_formula_says(kind, style):
                 ok = np.abs(want) < 3.38e38
             assert np.array_equal(np.isnan(kept), np.isnan(want)) and np.array_equal(np.sign(kept[~np.isnan(kept)]), np.sign(want[~np.isnan(want)]))
             assert np.isinf(kept[np.isinf(want)]).all() and (np.abs(kept[ok] - want[ok]) <= 2 * half * np.abs(want[ok]) + 2.0 ** -24).all()
+
+
+# ----------------------------------------------------------------------- attention: what single roundings leave --
+def run_one_head(cache, qx, table, lens, scale, window=0):
+    """qx [n_seq, n_tok, heads * dim] over one kv head, and the workspace it leaves."""
+    k, v, ks, vs = cache.device()
+    c = q.KvCache(base.KINDS[cache.kind], k, v, ks, vs)
+    n_seq, n_tok, width = qx.shape
+    ws = torch.zeros(q.attn_ws_bytes(c, width // cache.dim, n_seq, n_tok, table.shape[1]), dtype=torch.uint8, device="cuda")
+    out = torch.full(qx.shape, float("nan"), device="cuda")
+    q.attn_decode(q.AttnArgs(c, dev(qx), out, dev(table), dev(np.array(lens, np.int32)), ws, scale, window))
+    return out.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("typical", [0.01, 1e-5])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 65504.0, -65504.0])
+@pytest.mark.parametrize("group", [1, 3])
+def test_attn_scales_a_query_does_not_see_change_nothing(dim, typical, bad, group):
+    """Q8_0, eight tokens, a window: slots that only some of the queries see have scales far from all others'."""
+    rng = np.random.default_rng(dim)
+    n, n_tok, page, window = 44, 8, 16, 30
+    cache = ref.Cache(rng, "q8", 3, 1, page, dim)
+    table = np.array([[2, 0, 1]], np.int32)
+    for i in range(2):
+        cache.scale[i][:] = torch.from_numpy(typical * rng.uniform(0.5, 1, cache.scale[i].shape)).half()
+    seen = [[np.arange(p - window + 1, p + 1) for p in range(n - n_tok, n)]]
+    x = np.zeros((1, n_tok, group, dim), np.float32)
+    at = rng.integers(0, dim, (n_tok, group))
+    for t in range(n_tok):
+        for g in range(group):
+            x[0, t, g, at[t, g]] = rng.uniform(0.5, 1) / (127 * typical)
+    x = x.reshape(1, n_tok, -1)
+    want, tol = tight.attn(cache, x, table, [n], 1.0, seen=seen, depth=8)
+    first = seen[0][0][0]                               # the first slots of the first queries, the last ones of the last
+    for j in (first, first + 1, n - 2, n - 1):
+        for i in range(2):
+            cache.scale[i][table[0, j // page], 0, j % page] = bad
+    got = run_one_head(cache, x, table, [n], 1.0, window)
+    clear = slice(2, n_tok - 2)                         # queries that see none of these
+    assert (np.abs(got[:, clear] - want[:, clear]) <= tol[:, clear]).all(), np.max(np.abs(got - want)[:, clear] / tol[:, clear])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("n_tok,group", [(1, 1), (1, 8), (4, 3)])
+def test_attn_a_large_scale_of_little_weight_leaves_the_others_exact(dim, n_tok, group):
+    """Q8_0: the first slot's values are up to 65504 times 127, its weight is about 2^-40."""
+    rng = np.random.default_rng(dim + n_tok)
+    n, page = 30, 16
+    cache = ref.Cache(rng, "q8", 2, 1, page, dim)
+    table = np.array([[1, 0]], np.int32)
+    cache.scale[1][:] = torch.from_numpy(1e-4 * rng.uniform(0.5, 1, cache.scale[1].shape)).half()
+    cache.scale[1][1, 0, 0] = 65504.0
+    x = np.zeros((1, n_tok, group, dim), np.float32)
+    x[..., 5] = 1.0
+    x = x.reshape(1, n_tok, -1)
+    cache.kv[0][:, :, :, 5] = torch.from_numpy(rng.integers(-20, 20, (2, 1, page))).to(torch.int8)
+    cache.scale[0][:, :, :, 0] = 2.0 ** -5
+    cache.kv[0][1, 0, 0, 5] = -127
+    cache.scale[0][1, 0, 0, 0] = 0.2185                 # a score of -27.75, 40 halvings
+    want, tol = tight.attn(cache, x, table, [n], 1.0, depth=8)
+    got = run_one_head(cache, x, table, [n], 1.0)
+    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
