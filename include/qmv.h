@@ -390,11 +390,13 @@ int kv_append(const qmv_append *a, qmv_stream_t stream);
  * multiple of n_kv_head, 1 <= n_head / n_kv_head * n_tok <= 1024.  The longest
  * lengths, in steps of 64 slots, over all sequences and heads stay below 2^31.
  * Sums, maxima and products are f32; q and the weights reach the tensor cores
- * as sums of two f16 parts (f16 and Q8_0 caches: 22 bits, q's of the row's
- * largest value) or three bf16 parts (24 bits).  For Q8_0 it is a weight's
- * product with a block's scale that is split; what the parts leave is at most
- * 2^-23 of the product or 2^-39 of the largest one among the query's 32
- * neighbouring slots.  Weighted sums are divided by
+ * as sums of two f16 parts (f16 and Q8_0 caches) or three bf16 parts (24 bits).
+ * What two parts leave of q's values is at most 2^-23 of the row's largest one;
+ * of a weight at most 2^-23 of it or 2^-45 of the query's largest one, whichever
+ * is more.  For Q8_0 it is a weight's product with a block's scale that is split:
+ * at most 2^-23 of it or 2^-39 of the largest product among the query's 32
+ * neighbouring slots.  (All for rows of q whose largest value is 2^-100 or more;
+ * scores have to stay within f32's range.)  Weighted sums are divided by
  * the weights' sum at the end: values above 2^100 may overflow on the way.
  * The work of all sequences and heads is cut into equal shares, one per CTA;
  * sequences that several CTAs share are joined by the last one to finish, in a fixed

@@ -26,8 +26,11 @@
 // of the CTA, and 8 rows fill the instruction.  The weights turn from the first
 // product's C layout to the second's B layout by movmatrix.  f32 operands are
 // split into parts that the tensor core multiplies exactly:
-//   f16 cache:   q * 2^e (per row, so that the largest value is below 2^13) and
-//                2^9 * p as two f16 parts: 22 bits;
+//   f16 cache:   q * 2^e (per row, so that the largest value is below 2^13) as two
+//                f16 parts, 22 bits; 2^9 * p as one and 2^11 times what it leaves
+//                as another, in two products: 22 bits of weights down to 2^-22 of
+//                the largest (with a second part without a factor 12 bits are left there,
+//                alike for alike weights, so that a long tail's errors add up);
 //   bf16 cache:  q and p as three bf16 parts, 24 bits;
 //   Q8_0 cache:  q as for f16 (int8 is exact in it), and p * scale as two f16
 //                parts times a power of two of its own for every row, tile and
@@ -73,12 +76,13 @@ constexpr int ATT_MIN_NW = 4;
 // 16 sequences 105 -> 88 us, but 16 rows of them 82 -> 112 us.
 __host__ __device__ constexpr int attn_tile(int type, int dp, int mb) { return dp <= 64 || (type == 2 && dp <= 128 && mb == 1) ? 32 : 16; }
 constexpr int ATT_MIN_TILE = 16, ATT_MAX_TILE = 32;
-// log2 of how far a weight may pass 1, and of the factor of the weights in f16
-// parts: together below 2^16, and the second keeps what an f16 part cuts off
-// (half a step of its subnormals) below 2^-34 of the reference.  bf16 parts
-// have f32's range.
+// log2 of how far a weight may pass 1, and of the factors of an f16 cache's
+// weights and of what their first part leaves of them (half a step at most):
+// either stays below 2^15, and half a step of the second part's subnormals is
+// 2^-45 of the reference.  Other caches' weights keep f32's range.
 __host__ __device__ constexpr float attn_slack(int type) { return type == 0 ? 6.f : 12.f; }
 constexpr float ATT_F16_SHIFT = 9.f;
+constexpr float ATT_F16_LEFT = 2048.f;
 
 // 8-row blocks that one CTA takes: up to 2.  (With 4, whose outputs and operands
 // leave no registers to overlap anything, 32 rows over 4096 slots of 4 sequences
@@ -244,12 +248,13 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// (x, y) as two f16 parts / three bf16 parts, packed pairwise.
+// (x, y) as two f16 parts (the second times LEFT) / three bf16 parts, packed pairwise.
+template <int LEFT = 1>
 __device__ __forceinline__ void split_f16(float x, float y, uint32_t &hi, uint32_t &lo)
 {
     const __half2 h = __floats2half2_rn(x, y);
     const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+    const __half2 l = __floats2half2_rn((x - f.x) * LEFT, (y - f.y) * LEFT);
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
@@ -964,18 +969,29 @@ __global__ void __launch_bounds__(AttnGeom<TYPE, DP, MB>::THREADS, AttnGeom<TYPE
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             uint32_t w[3];
-                            if constexpr (TYPE == KV_F16) split_f16(sc[nb][u][2 * i], sc[nb][u][2 * i + 1], w[0], w[1]);
+                            if constexpr (TYPE == KV_F16) split_f16<(int)ATT_F16_LEFT>(sc[nb][u][2 * i], sc[nb][u][2 * i + 1], w[0], w[1]);
                             else split_bf16(sc[nb][u][2 * i], sc[nb][u][2 * i + 1], w[0], w[1], w[2]);
 #pragma unroll
                             for (int k = 0; k < NPP; ++k) pb[nb][u][k][i] = movm_t(w[k]);
                         }
-                auto product = [&](float (&t)[4], const uint32_t (&r)[SUB][4], int nb) {     // the small parts first
-                    mma_16_0<PBF>(t, r[0], pb[nb][0][NPP - 1][0], pb[nb][0][NPP - 1][1]);
+                auto chain = [&](float (&t)[4], const uint32_t (&r)[SUB][4], int nb, int k0, int k1) {     // parts k0 down to k1
+                    mma_16_0<PBF>(t, r[0], pb[nb][0][k0][0], pb[nb][0][k0][1]);
 #pragma unroll
-                    for (int k = NPP - 1; k >= 0; --k)
+                    for (int k = k0; k >= k1; --k)
 #pragma unroll
                         for (int u = 0; u < SUB; ++u)
-                            if (k < NPP - 1 || u > 0) mma_16<PBF>(t, r[u], pb[nb][u][k][0], pb[nb][u][k][1]);
+                            if (k < k0 || u > 0) mma_16<PBF>(t, r[u], pb[nb][u][k][0], pb[nb][u][k][1]);
+                };
+                auto product = [&](float (&t)[4], const uint32_t (&r)[SUB][4], int nb) {
+                    if constexpr (TYPE == KV_F16) {
+                        float left[4];
+                        chain(left, r, nb, 1, 1);
+                        chain(t, r, nb, 0, 0);
+                        fma2(t[0], t[1], left[0], left[1], 1.f / ATT_F16_LEFT);
+                        fma2(t[2], t[3], left[2], left[3], 1.f / ATT_F16_LEFT);
+                    } else {
+                        chain(t, r, nb, NPP - 1, 0);
+                    }
                 };
                 auto values = [&](auto &&each) {
 #pragma unroll

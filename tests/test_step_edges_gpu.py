@@ -237,3 +237,16 @@ def test_attn_a_large_scale_of_little_weight_leaves_the_others_exact(dim, n_tok,
     want, tol = tight.attn(cache, x, table, [n], 1.0, depth=8)
     got = run_one_head(cache, x, table, [n], 1.0)
     assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
+
+
+@pytest.mark.parametrize("kind,dim", [(k, d) for k in ("f16", "bf16", "q8") for d in (32, 64, 128, 256) if (k, d) != ("q8", 32)])
+@pytest.mark.parametrize("group,n_seq", [(1, 1), (1, 900), (16, 900)])
+def test_attn_a_long_tail_of_small_weights_keeps_its_sum(kind, dim, group, n_seq):
+    """700 slots of about 2^-22 of the first ones' weight: their errors are alike and add up.  Many sequences share the
+    pages, so that a CTA runs over whole ones."""
+    n = 700
+    cache, table, lens, x = tight.long_tail(kind, dim, n)
+    x = np.tile(x, (1, 1, group))
+    want, tol = tight.attn(cache, x, table, lens, 1.0, depth=100)
+    got = run_one_head(cache, np.tile(x, (n_seq, 1, 1)), np.tile(table, (n_seq, 1)), lens * n_seq, 1.0)
+    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
