@@ -250,3 +250,48 @@ def test_attn_a_long_tail_of_small_weights_keeps_its_sum(kind, dim, group, n_seq
     want, tol = tight.attn(cache, x, table, lens, 1.0, depth=100)
     got = run_one_head(cache, np.tile(x, (n_seq, 1, 1)), np.tile(table, (n_seq, 1)), lens * n_seq, 1.0)
     assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
+
+
+@pytest.mark.parametrize("kind,dim", [("f16", 16), ("f16", 64), ("f16", 128), ("f16", 256), ("bf16", 64), ("bf16", 128), ("bf16", 256), ("q8", 64), ("q8", 128), ("q8", 256)])
+@pytest.mark.parametrize("group", [1, 8, 16])
+def test_attn_two_slots_keep_every_part(kind, dim, group):
+    """Bounds of a few roundings, which a lost part of a query or a weight passes many times over."""
+    rng = np.random.default_rng(dim + group)
+    cache, table, lens, x = tight.two_slots(rng, kind, dim, 50, group)
+    want, tol = tight.attn(cache, x, table, lens, 1.0)
+    got = run_one_head(cache, x, table, lens, 1.0)
+    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / np.maximum(tol, 1e-30))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "q8"])
+@pytest.mark.parametrize("n_kv,n_seq", [(8, 20), (1, 1)])
+def test_attn_every_counter_is_zero_again(kind, n_kv, n_seq):
+    """64 wide with one query: as many CTAs as an instance can have, nearly all of them with a segment that they share."""
+    rng = np.random.default_rng(n_kv)
+    lens = [int(x) for x in rng.integers(2500, 3500, n_seq)] if n_seq > 1 else [60000]
+    table, n_pages = make_tables(rng, lens, 64)
+    cache = ref.Cache(rng, kind, n_pages, n_kv, 64, 64)
+    k, v, ks, vs = cache.device()
+    c = q.KvCache(base.KINDS[kind], k, v, ks, vs)
+    x = dev(rng.standard_normal((n_seq, 1, n_kv * 64)).astype(np.float32))
+    ws = torch.zeros(q.attn_ws_bytes(c, n_kv, n_seq, 1, table.shape[1]), dtype=torch.uint8, device="cuda")
+    tab, n, first = dev(table), dev(np.array(lens, np.int32)), None
+    for _ in range(4):
+        out = torch.full(x.shape, float("nan"), device="cuda")
+        q.attn_decode(q.AttnArgs(c, x, out, tab, n, ws, 0.125))
+        torch.cuda.synchronize()
+        assert int(ws[:480 * 4].sum()) == 0             # the counters of the most CTAs that a call has
+        first = out if first is None else first
+        assert torch.equal(first, out) and bool(torch.isfinite(out).all())
+
+
+# --------------------------------------------------------------------------------------------------------- eviction --
+def test_evict_long_caches_beyond_the_keys_of_a_cluster():
+    """Eight CTAs hold the keys of 327680 slots; the others are made anew in every round."""
+    n = 330000
+    rng = np.random.default_rng(5)
+    z = rng.standard_normal((1, 1, n)).astype(np.float32)
+    z[rng.random(z.shape) < 0.01] = np.nan
+    z[rng.random(z.shape) < 0.01] = -np.inf
+    base.run_evict("f16", 16, 1, 256, [n], 4, 100, 2000, z)
+    base.run_evict("f16", 16, 1, 256, [n], 0, 0, 1500, rng.integers(0, 4, (1, 1, n)).astype(np.float32))      # ties

@@ -2,10 +2,13 @@
 argument object lets a call touch, and which mistakes the tests' bounds tell apart."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
 import quantized_decode_superblocks_b200 as q
+import step_ref as ref
+import step_tight as tight
 from test_step_host import A, SHAPE, L, attn, evict, good  # noqa: F401
 
 
@@ -74,3 +77,37 @@ def test_score_rows_may_not_reach_into_each_other(L):  # noqa: F811
     # outputs may lie between the rows' entries' end and the buffer's
     end = A + (15 * 64 + 20) * 4
     assert evict(L, score_slots=20, score_out=end - 4) == SHAPE and good(L, evict, score_slots=20, score_out=end)
+
+
+# --------------------------------------------------------------- the bounds that the GPU tests hold the kernels to --
+@pytest.mark.parametrize("kind,dim", [("f16", 16), ("f16", 128), ("bf16", 64), ("bf16", 256), ("q8", 64), ("q8", 256)])
+@pytest.mark.parametrize("slip", ["q", "weights"])
+def test_a_lost_part_of_queries_or_weights_breaks_the_bound(kind, dim, slip):
+    rng = np.random.default_rng(dim)
+    cache, table, lens, x = tight.two_slots(rng, kind, dim, 50, 3)
+    want, tol = tight.attn(cache, x, table, lens, 1.0)
+    wrong, _ = tight.attn(cache, x, table, lens, 1.0, slip)
+    beyond = np.abs(wrong - want) > 2 * tol
+    # f16 parts: 2^-12 against some 40 roundings of 2^-24; the third bf16 part: 2^-16 against some 20
+    assert beyond.mean() > (0.2 if kind == "bf16" else 0.7)
+
+
+@pytest.mark.parametrize("kind", ["f16", "q8"])
+def test_a_long_tail_cut_at_the_second_parts_last_bit_breaks_the_bound(kind):
+    cache, table, lens, x = tight.long_tail(kind, 64, 700)
+    want, tol = tight.attn(cache, x, table, lens, 1.0, depth=100)
+    p = 2.0 ** 9 * np.exp(np.float64(x[0, 0, 3]))
+    hi = tight.high_part(p, "f16")
+    kept = (hi + tight.high_part(p - hi, "f16")) / p
+    assert (np.abs(want * kept - want) > 5 * tol).all()
+    scaled = (hi + tight.high_part(p - hi, "f16", 2048)) / p
+    assert (np.abs(want * scaled - want) < 0.01 * tol).all()
+
+
+def test_plain_one_hot_attention_agrees_with_the_general_form():
+    for kind in ("f16", "bf16", "q8"):
+        rng = np.random.default_rng(4)
+        cache, table, lens, x = tight.two_slots(rng, kind, 64, 6, 2)
+        a, small = tight.attn(cache, x, table, lens, 1.0)
+        b, large, _, _ = ref.attn(cache, x, 2, table, lens, 1.0)
+        assert np.abs(a - b).max() < 1e-14 and (small <= large + 1e-30).all()
