@@ -388,7 +388,7 @@ int kv_append(const qmv_append *a, qmv_stream_t stream);
  * q, out: f32, apart from each other, 16- and 4-byte aligned, token s * n_tok + t at + (s * n_tok + t) *
  * stride floats (q_stride a multiple of 4), heads one after another; n_head a
  * multiple of n_kv_head, 1 <= n_head / n_kv_head * n_tok <= 1024.  The longest
- * lengths, in steps of 64 slots, over all sequences and heads stay below 2^31.
+ * lengths, in steps of 64 slots, over all sequences and heads stay below 2^30.
  * Sums, maxima and products are f32; q and the weights reach the tensor cores
  * as sums of two f16 parts (f16 and Q8_0 caches) or three bf16 parts (24 bits).
  * What two parts leave of q's values is at most 2^-23 of the row's largest one;

@@ -85,7 +85,7 @@ int attn_ws(int type, int head_dim, int n_kv, int n_head, int n_seq, int n_tok, 
     if (rows > MAX_GROUP_ROWS) return QMV_ERR_SHAPE;
     const int mb = attn_mb(rows);
     w.steps = ceil_div(rows, 8 * mb) * n_seq * n_kv * (slots / (ATT_MIN_TILE * ATT_MIN_NW) + 2);
-    if (w.steps > INT_MAX) return QMV_ERR_SHAPE;
+    if (w.steps > INT_MAX / 2) return QMV_ERR_SHAPE;       // step numbers are 32-bit, and whole shares may pad them by an eighth
     const size_t parts = (size_t)2 * ATT_MAX_CTAS * 8 * mb;
     w.raw_stride = ceil_div(slots, ATT_MAX_TILE) * ATT_MAX_TILE;
     w.raw_rows = ceil_div(rows, 2) * 2;

@@ -9,6 +9,7 @@ import torch
 import quantized_decode_superblocks_b200 as q
 import step_ref as ref
 import step_tight as tight
+import test_step_host as host
 from test_step_host import A, SHAPE, L, attn, evict, good  # noqa: F401
 
 
@@ -77,6 +78,20 @@ def test_score_rows_may_not_reach_into_each_other(L):  # noqa: F811
     # outputs may lie between the rows' entries' end and the buffer's
     end = A + (15 * 64 + 20) * 4
     assert evict(L, score_slots=20, score_out=end - 4) == SHAPE and good(L, evict, score_slots=20, score_out=end)
+
+
+def test_attn_steps_leave_room_for_padding(L):  # noqa: F811
+    """Step numbers are 32-bit; a CTA's share may grow by an eighth and one to end with a sequence."""
+    def padded(steps, ctas):
+        share = -(-steps // ctas)
+        return (share + share // 8 + 1) * ctas
+    assert padded(2 ** 31 - 1, 444) >= 2 ** 31 and padded(2 ** 30, 444) < 2 ** 31
+    c = host.cache(n_kv_head=1024, head_dim=16, page_stride=1024 * 16 * 16, head_stride=256, slot_stride=16)
+    assert q.attn_ws_bytes(c, 1024, 1, 1, 2 ** 22) == 0        # 1024 heads, 2^26 slots, 64 a step
+    assert q.attn_ws_bytes(c, 1024, 1, 1, 2 ** 22 - 2 ** 12) > 0
+    kw = dict(c=c, n_head=1024, n_seq=1, q_stride=16384, out_stride=16384)
+    assert attn(L, max_pages=2 ** 22, table_stride=2 ** 22, **kw) == SHAPE
+    assert good(L, attn, max_pages=2 ** 21, table_stride=2 ** 21, **kw)
 
 
 # --------------------------------------------------------------- the bounds that the GPU tests hold the kernels to --
