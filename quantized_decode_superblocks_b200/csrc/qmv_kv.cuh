@@ -417,7 +417,8 @@ static __global__ void __launch_bounds__(EV_COPY_THREADS) kv_evict_copy_kernel(c
     const int h = blockIdx.x % p.n_kv, s = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int m = min(min(max(__ldg(p.kv_len + s), 0), p.max_len), p.budget);
     const int i = (blockIdx.x / p.n_kv * (EV_COPY_THREADS / 32) + warp) * EV_SLOTS + lane % EV_SLOTS;
-    const bool in = lane < 2 * EV_SLOTS && i < m;
+    static_assert(2 * EV_SLOTS == 32, "a lane per row of k or v");
+    const bool in = i < m;
     const int di = page_of(i, p), pd = in ? __ldg(p.dst_table + (int64_t)s * p.dst_table_stride + di) : -1;
     const uint32_t bar = smem_addr(s_bar + warp);
     if (lane == 0) {

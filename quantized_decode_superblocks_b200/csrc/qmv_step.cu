@@ -68,7 +68,6 @@ int page_shift(int page_size)
     return s;
 }
 
-
 struct AttnWs {
     size_t ml, o, raw, stats, bytes;
     int64_t raw_stride, raw_rows;
@@ -76,9 +75,8 @@ struct AttnWs {
 };
 
 // Workspace: counters | parts' (m, l) | parts' outputs | raw scores | rows' (m, l)
-int attn_ws(int type, int head_dim, int n_kv, int n_head, int n_seq, int n_tok, int64_t slots, bool score, AttnWs &w)
+int attn_ws(int head_dim, int n_kv, int n_head, int n_seq, int n_tok, int64_t slots, bool score, AttnWs &w)
 {
-    (void)type;
     if (n_tok < 1 || n_tok > QMV_MAX_NTOK) return QMV_ERR_NTOK;
     if (n_head < 1 || n_head > MAX_HEADS || n_head % n_kv) return QMV_ERR_SHAPE;
     const int rows = n_head / n_kv * n_tok;
@@ -117,7 +115,7 @@ size_t attn_ws_bytes(const qmv_kv_cache *cache, int n_head, int n_seq, int n_tok
     int64_t slots = 0;
     AttnWs w;
     if (check_table(*cache, n_seq, max_pages, max_pages, &slots) != QMV_OK ||
-        attn_ws(cache->type, cache->head_dim, cache->n_kv_head, n_head, n_seq, n_tok, slots, with_score != 0, w) != QMV_OK) return 0;
+        attn_ws(cache->head_dim, cache->n_kv_head, n_head, n_seq, n_tok, slots, with_score != 0, w) != QMV_OK) return 0;
     return w.bytes;
 }
 
@@ -132,7 +130,7 @@ int attn_decode(const qmv_attn *a, qmv_stream_t stream)
     AttnWs w;
     if (a->n_tok < 1 || a->n_tok > QMV_MAX_NTOK) return QMV_ERR_NTOK;
     if ((rc = check_table(c, a->n_seq, a->max_pages, a->table_stride, &slots))) return rc;
-    if ((rc = attn_ws(c.type, c.head_dim, c.n_kv_head, a->n_head, a->n_seq, a->n_tok, slots, a->score != nullptr, w))) return rc;
+    if ((rc = attn_ws(c.head_dim, c.n_kv_head, a->n_head, a->n_seq, a->n_tok, slots, a->score != nullptr, w))) return rc;
     const int64_t width = (int64_t)a->n_head * c.head_dim;
     if (!stride_ok(a->q_stride, width) || !stride_ok(a->out_stride, width) || (a->score && !score_ok(a->score_stride, a->score_slots))) return QMV_ERR_SHAPE;
     if (a->window < 0 || a->n_sink < 0 || !(a->scale - a->scale == 0.f)) return QMV_ERR_SHAPE;
