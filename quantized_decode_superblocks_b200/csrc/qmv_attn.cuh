@@ -70,11 +70,12 @@ enum { KV_F16 = 0, KV_BF16 = 1, KV_Q8_0 = 2 };
 // Warps of a CTA; 6 where a stage is 16 KB and one CTA fills the SM.
 __host__ __device__ constexpr int attn_warps(int type, int dp) { return dp > 128 && type != 2 ? 6 : 4; }
 constexpr int ATT_MIN_NW = 4;
-// Slots of a tile: 32 where its keys and values are short and registers allow, so
-// that a warp's work around a tile is spread over more of them.  Against 16: f16,
-// 64 wide, one token over 131071 slots 60 -> 54 us; Q8_0, 128 wide, one token for
-// 16 sequences 105 -> 88 us, but 16 rows of them 82 -> 112 us.
-__host__ __device__ constexpr int attn_tile(int type, int dp, int mb) { return dp <= 64 || (type == 2 && dp <= 128 && mb == 1) ? 32 : 16; }
+// Slots of a tile: 32 where its keys and values are short, so that a warp's work
+// around a tile is spread over more of them.  Against 16 (32 query / 8 kv heads):
+// f16, 64 wide, one token over 131071 slots 47.9 -> 46.4 us; Q8_0, 128 wide, for
+// sequences of 3000 to 16000 slots, one token of 16 98 -> 84 us, four tokens of 8
+// (two CTAs of two stages instead of three of three) 83 -> 70 us.
+__host__ __device__ constexpr int attn_tile(int type, int dp) { return dp <= 64 || (type == 2 && dp <= 128) ? 32 : 16; }
 constexpr int ATT_MIN_TILE = 16, ATT_MAX_TILE = 32;
 // log2 of how far a weight may pass 1, and of the factors of an f16 cache's
 // weights and of what their first part leaves of them (half a step at most):
@@ -86,7 +87,7 @@ constexpr float ATT_F16_LEFT = 2048.f;
 
 // 8-row blocks that one CTA takes: up to 2.  (With 4, whose outputs and operands
 // leave no registers to overlap anything, 32 rows over 4096 slots of 4 sequences
-// take 74 us instead of 45 us in bf16 and 53 us instead of 43 us in Q8_0, 128 wide.)
+// take 48 us instead of 36 us in bf16 and 48 us instead of 38 us in Q8_0, 128 wide.)
 __host__ __device__ constexpr int attn_mb(int rows) { return rows <= 8 ? 1 : 2; }
 constexpr int ATT_MAX_SEQ = 1024;
 constexpr int ATT_MAX_CTAS = 480;            // bound for the workspace's parts
@@ -321,7 +322,7 @@ __device__ __forceinline__ void i8_to_f16(uint32_t w, uint32_t &p0, uint32_t &p1
 // Shared-memory geometry of one instance: MB 8-row blocks of a DP-wide head.
 template <int TYPE, int DP, int MB>
 struct AttnGeom {
-    static constexpr int TILE = attn_tile(TYPE, DP, MB), SUB = TILE / 16;     // slots of a tile, and products of 16
+    static constexpr int TILE = attn_tile(TYPE, DP), SUB = TILE / 16;     // slots of a tile, and products of 16
     static constexpr uint32_t ALL = 0xFFFFFFFFu >> (32 - TILE);
     static constexpr int EB = TYPE == KV_Q8_0 ? 1 : 2;           // bytes of a value
     static constexpr int PITCH = DP * EB;                        // bytes of a slot's k (or v)
@@ -332,14 +333,15 @@ struct AttnGeom {
     static constexpr int STAGE = 2 * (KV_BYTES + SC_BYTES);      // one warp's stage: k | v | k scales | v scales
     static constexpr int ROWS = 8 * MB;
     static constexpr int NW = attn_warps(TYPE, DP), THREADS = NW * 32;
-    // Stages and CTAs a SM: three CTAs with up to 70 KB of shared memory where the
-    // registers allow it (narrow heads) or the arithmetic of Q8_0 needs the warps,
-    // else two with about 96 KB of ring, one where a stage is 16 KB.  Three against
-    // two: f16, 64 wide, one token over 131071 slots 53.5 -> 51.4 us, 32 rows 20.7 ->
-    // 18.7 us; Q8_0, 128 wide, 8 tokens 43.0 -> 41.0 us; but 64 wide, 16 rows 25 ->
-    // 37 us, and f16, 128 wide, 16 rows (two stages left) 46 -> 66 us.
-    static constexpr bool THREE = (DP <= 64 && (MB == 1 || DP <= 32 || TYPE == KV_F16)) || (TYPE == KV_Q8_0 && DP == 128);
-    static constexpr int NST = DP > 128 ? 2 : THREE ? (STAGE >= 8 * 1024 ? 2 : DP == 128 ? 3 : 4) : STAGE >= 8 * 1024 ? 3 : 5;
+    // Stages and CTAs a SM: three CTAs with up to 70 KB of shared memory for narrow
+    // heads and one row block of Q8_0, else two with up to 110 KB, one where a stage
+    // is 16 KB.  Three against two (32 query / 8 kv heads): f16, 64 wide, one token
+    // over 131071 slots 47.5 -> 46.4 us, 8 tokens over 4096 slots of 4 sequences 20.2
+    // -> 19.2 us; Q8_0, 128 wide, one token for 16 sequences 84 us either way.  bf16,
+    // 64 wide, 16 rows have two, the 8 tokens 23.9 us (22.4 us with three); 16 rows
+    // of Q8_0 or of 128 wide heads do not fit three times.
+    static constexpr bool THREE = (DP <= 64 && (MB == 1 || DP <= 32 || TYPE == KV_F16)) || (TYPE == KV_Q8_0 && DP == 128 && MB == 1);
+    static constexpr int NST = DP > 128 ? 2 : THREE ? (STAGE >= 8 * 1024 ? 2 : 4) : STAGE > 8 * 1024 ? 2 : STAGE == 8 * 1024 ? 3 : 5;
     static constexpr int RING = NW * NST * STAGE;
     static constexpr int NPQ = TYPE == KV_BF16 ? 3 : 2;          // parts of q
     static constexpr int NPP = TYPE == KV_BF16 ? 3 : 2;          // parts of the weights
