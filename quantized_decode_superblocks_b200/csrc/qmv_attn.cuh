@@ -50,10 +50,11 @@
 // among the values (Q8_0: the scales) are made finite first.
 //
 // Measured (32 query / 8 kv heads): f16, 64 wide, one token over 131071 slots
-// 46 us, 5.8 TB/s; bf16, 128 wide, 32 ragged sequences up to 16384 slots 177 us,
-// 6.6 TB/s, both bound by DRAM; Q8_0, 128 wide, 8 tokens over 4096 slots of 4 sequences
-// 39 us, bound by instructions; one token over 1000 slots 5.6 us, bound by
-// the memory round trips that wait on each other.
+// 46.5 us, 5.8 TB/s; bf16, 128 wide, 32 ragged sequences up to 16384 slots 181 us,
+// 6.5 TB/s, both bound by DRAM; Q8_0, 128 wide, 8 tokens over 4096 slots of 4 sequences
+// 38 us, bound by dependent chains of instructions on under two warps a scheduler
+// (0.41 issued a cycle); one token over 1000 slots 5.6 us, bound by the memory
+// round trips that wait on each other.
 #pragma once
 
 #include <type_traits>
