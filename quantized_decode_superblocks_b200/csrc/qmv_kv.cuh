@@ -16,7 +16,7 @@ __device__ __forceinline__ int page_of(int slot, const Params &p) { return p.pag
 // One CTA per (token, share of the heads): the token's cosines and sines once
 // in 64 bits, then one warp per head, whose first head is loaded meanwhile.  A
 // few KB per token: one token of 32/8 heads of 64 takes 2.4 us, launch and memory
-// latency; 64 x 4 tokens of 32/8 heads of 128, bf16, 5.3 us (1.8 us of bytes), the
+// latency; 64 x 4 tokens of 32/8 heads of 128, bf16, 5.2 us (1.8 us of bytes), the
 // instructions of a head.
 constexpr int APP_THREADS = 128, APP_CTAS = 4;     // CTAs on a SM
 
@@ -33,12 +33,13 @@ __device__ __forceinline__ float4 rope_turn(double pos, float f)
 }
 
 // a c + b s, rounded once: the products' and the sum's roundings are caught in f32.  Infinities, also those of
-// a sum beyond f32's range, and NaN are final: what they leave would be infinity minus infinity.
+// a sum beyond f32's range, are final: what they leave is a NaN (infinity minus infinity), which the minimum
+// passes over for a number that changes neither them nor a NaN.
 __device__ __forceinline__ float rope_sum(float a, float b, float4 t)
 {
     const float p = a * t.x, q = b * t.z, r = p + q, v = r - p;
     const float left = fmaf(a, t.y, fmaf(a, t.x, -p)) + fmaf(b, t.w, fmaf(b, t.z, -q));
-    return fabsf(r) < INFINITY ? r + (((p - (r - v)) + (q - v)) + left) : r;
+    return r + fminf(((p - (r - v)) + (q - v)) + left, 3.402823466e38f);
 }
 
 struct AppendParams {
